@@ -306,6 +306,133 @@ int dense_head_static(const void* E, int64_t v, int32_t d, int32_t dtype,
                       float* out_lse, void* stream);
 
 /*
+ * Around the head in a decode step: the norm in front of it, the dense head
+ * with E and h in 8 bits, and the verification of drafted tokens.
+ *
+ * 8-bit values are e4m3 (4 exponent bits, 3 mantissa bits, largest 448, no
+ * infinity).  A block of 128 columns of a row of h, or of 128 x 128 of E (cut
+ * at the matrix's ends), has one fp32 scale max(max|y| / 448, 2^-126); a code
+ * is the e4m3 of y / scale, to nearest, ties to even, and stands for code *
+ * scale.  Strides are in elements and need at least the columns of a row;
+ * with one row a stride is not looked at.  Zero rows (or sequences) are
+ * allowed and do nothing.  Unlike the other calls these take matrices of any
+ * number of rows.
+ */
+#define FH_MAX_NORM_D 8192 /* columns of flashhead_rmsnorm */
+
+/*
+ * RMS norm with the residual's addition, per row:
+ *   t = x + residual
+ *   y = t / sqrt(mean(t^2) + eps) * (weight_offset + weight)
+ * in fp32, each output rounded once (y is made from the unrounded t).
+ *   x             device, rows x d, dtype FH_DTYPE_*, d <= FH_MAX_NORM_D
+ *   residual      device, rows x d, or NULL (t = x)
+ *   weight        device, d, or NULL (ones)
+ *   eps           finite, >= 0;  weight_offset finite (0, or 1 for weights
+ *                 that are stored as their difference from one)
+ *   residual_out  device, rows x d, t, or NULL
+ *   y             device, rows x d, or NULL
+ *   y8, y_scale   device, rows x d codes and rows x ceil(d / 128) scales of
+ *                 y (of its fp32 value), or both NULL
+ * One of the outputs must be given.  residual_out and y may each be x or
+ * residual themselves (the same address and stride); no other overlap is
+ * allowed.  Rows of x, residual, weight, residual_out and y start at multiples
+ * of 16 bytes and are multiples of 16 bytes long; rows of y8 start at
+ * multiples of 8 bytes (dtype bf16) or 4 (fp32).  rows < 2^24.  The mean of
+ * the squares is an fp32 sum: |t| up to about 1e18.
+ */
+int flashhead_rmsnorm(const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                      const void* weight, int64_t rows, int32_t d, int32_t dtype, float eps,
+                      float weight_offset, void* residual_out, int64_t ldro, void* y, int64_t ldy,
+                      uint8_t* y8, int64_t ldy8, float* y_scale, int64_t lds, void* stream);
+
+/*
+ * E in 8 bits: the codes and the scales of its 128 x 128 blocks (a step of
+ * loading a model; E is not needed by dense_logits_fp8 afterwards).
+ *   E        device, v x d, dtype FH_DTYPE_*, 16-byte rows as for dense_head
+ *   E8       device, v x d codes, aligned as y8 above
+ *   E_scale  device, ceil(v / 128) x ceil(d / 128)
+ * No overlap is allowed.  v <= 65535 * 128.
+ */
+int flashhead_quantize_fp8(const void* E, int64_t v, int32_t d, int32_t dtype, int64_t lde,
+                           uint8_t* E8, int64_t lde8, float* E_scale, int64_t lds, void* stream);
+
+/*
+ * Logits of the dense head in 8 bits (Formula 1 over the values that the
+ * codes stand for):
+ *   out[m, t] = sum over k of h8[m, k] h_scale[m, k / 128]
+ *                             * E8[t, k] E_scale[t / 128, k / 128]
+ * with fp32 sums, rounded once to out_dtype.  Codes of the e4m3 NaN make the
+ * outputs of their row NaN.
+ *   h8, h_scale   device, rows x d and rows x ceil(d / 128)
+ *   E8, E_scale   device, v x d and ceil(v / 128) x ceil(d / 128)
+ *   d             a multiple of 16;  rows <= 65535 * 16
+ *   out           device, rows x v, FH_DTYPE_F32 or FH_DTYPE_BF16
+ * Rows of h8, E8 and out start at multiples of 16 bytes (v itself may be any
+ * size; columns [v, ldo) of out are left as they are).  The result does not
+ * depend on other rows, and a call is reproducible bit for bit.
+ */
+int dense_logits_fp8(const uint8_t* h8, int64_t ldh, const float* h_scale, int64_t lds,
+                     int32_t rows, const uint8_t* E8, int64_t lde, const float* E_scale,
+                     int64_t ldes, int64_t v, int32_t d, void* out, int32_t out_dtype, int64_t ldo,
+                     void* stream);
+
+/*
+ * Verification of drafted tokens (speculative decoding) for B sequences.
+ * Sequence s has the logits' rows row_start[s] .. row_start[s + 1] - 1: one
+ * for each of its n drafted tokens and one after them, so n = row_start[s + 1]
+ * - row_start[s] - 1 may be 0.  Its j-th draft is entry row_start[s] - s + j
+ * of draft_tokens, draft_probs and u_accept (the drafts of all sequences one
+ * after the other).  With p_j = softmax(logits / tau) at its row,
+ *   sample   draft x_j is accepted while u_accept[j] q_j(x_j) < p_j(x_j),
+ *            q_j its row of draft_probs, or 1 at x_j and 0 elsewhere when
+ *            draft_probs is NULL (a draft chosen without chance).  At the
+ *            first rejection the next token is drawn from max(p_j - q_j, 0)
+ *            (from p_j if that is zero everywhere); after n accepted drafts
+ *            from the last row's p.  A draw from weights w is the smallest t
+ *            with w_0 + .. + w_t > u_sample[s] * (w_0 + .. + w_{v-1}).
+ *   greedy   x_j is accepted while it is the lowest argmax of its row, which
+ *            is also the next token.
+ * The comparisons and sums are in fp64, so the result is the one the given
+ * numbers determine, on every call.  With n = 0 the call is a plain draw.
+ *   logits        device, rows x v, FH_DTYPE_*, rows at multiples of 16 bytes
+ *                 (v itself may be any size).  -inf marks a token that
+ *                 cannot occur.  A row of -inf alone, or with a NaN or +inf,
+ *                 has no distribution: a draft there is not accepted and the
+ *                 token drawn there is -1.
+ *   row_start     device, B + 1, not descending (may stop short of rows: rows
+ *                 outside every sequence are not used)
+ *   draft_tokens  device, n_drafts
+ *   draft_probs   device, n_drafts x v fp32 (>= 0, rows at multiples of 16
+ *                 bytes), or NULL; NULL in greedy mode.  A NaN counts as a
+ *                 weight of 0.
+ *   u_accept      device, n_drafts fp32 in [0, 1); u_sample device, B fp32 in
+ *                 [0, 1); both may be NULL in greedy mode
+ *   tau           finite, > 0 (greedy: not used)
+ *   max_tokens    columns of out_tokens and out_logp
+ *   out_tokens    device, B x max_tokens: the accepted drafts, then the next
+ *                 token, then -1
+ *   out_accepted  device, B: accepted drafts (the next token is at this
+ *                 column), or -1 for a sequence that cannot be read: no row,
+ *                 rows or drafts outside the arrays, a draft outside [0, v),
+ *                 or n >= max_tokens.  Its tokens are all -1.
+ *   out_logp      device, B x max_tokens: log p of each token (greedy: at tau
+ *                 = 1), 0 where the token is -1; or NULL
+ *   workspace     device, flashhead_verify_workspace_bytes(B, rows, v) bytes,
+ *                 16-byte aligned, one call in flight per workspace; its
+ *                 contents need no initialisation, and one made for more
+ *                 sequences or rows serves fewer.
+ * FH_ERR_INVALID_ARG for a workspace that is too small.
+ */
+size_t flashhead_verify_workspace_bytes(int32_t B, int64_t rows, int64_t v);
+int flashhead_verify(const void* logits, int64_t rows, int64_t v, int32_t dtype, int64_t ldl,
+                     const int32_t* row_start, int32_t B, const int32_t* draft_tokens,
+                     int64_t n_drafts, const float* draft_probs, int64_t ldq, int32_t mode,
+                     float tau, const float* u_accept, const float* u_sample, int32_t max_tokens,
+                     int32_t* out_tokens, int32_t* out_accepted, float* out_logp, void* workspace,
+                     size_t workspace_bytes, void* stream);
+
+/*
  * Equal-size spherical k-means (notes, Module 1; Formula 4, the summed
  * cosine of each token to its cluster's unit centroid; Formula 5, the
  * centroid is the unit-normalised mean of the cluster's rows): the offline

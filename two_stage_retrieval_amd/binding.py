@@ -47,8 +47,12 @@ EXPORTED = [
     "flashhead_mc_workspace_bytes", "flashhead_mc_marginal", "flashhead_kmeans",
     "flashhead_plan_step", "dense_head_static", "flashhead_trace_read",
     "flashhead_greedy_adaptive", "flashhead_sample_adaptive",
+    "flashhead_rmsnorm", "flashhead_quantize_fp8", "dense_logits_fp8",
+    "flashhead_verify_workspace_bytes", "flashhead_verify",
 ]
 FH_DENSE_STATIC_MAX_BATCH = 16
+FH_FP8_BLOCK = 128      # columns (and rows of E) that share a scale
+FH_MAX_NORM_D = 8192
 
 
 class fh_desc(C.Structure):
@@ -135,6 +139,19 @@ def _load() -> C.CDLL:
     lib.flashhead_plan_step.restype = C.c_int
     lib.flashhead_trace_read.argtypes = [vp, i64, C.POINTER(i64), C.POINTER(i64)]
     lib.flashhead_trace_read.restype = C.c_int
+    lib.flashhead_rmsnorm.argtypes = [vp, i64, vp, i64, vp, i64, i32, i32, f32, f32, vp, i64,
+                                      vp, i64, vp, i64, vp, i64, vp]
+    lib.flashhead_rmsnorm.restype = C.c_int
+    lib.flashhead_quantize_fp8.argtypes = [vp, i64, i32, i32, i64, vp, i64, vp, i64, vp]
+    lib.flashhead_quantize_fp8.restype = C.c_int
+    lib.dense_logits_fp8.argtypes = [vp, i64, vp, i64, i32, vp, i64, vp, i64, i64, i32, vp, i32,
+                                     i64, vp]
+    lib.dense_logits_fp8.restype = C.c_int
+    lib.flashhead_verify_workspace_bytes.argtypes = [i32, i64, i64]
+    lib.flashhead_verify_workspace_bytes.restype = C.c_size_t
+    lib.flashhead_verify.argtypes = [vp, i64, i64, i32, i64, vp, i32, vp, i64, vp, i64, i32, f32,
+                                     vp, vp, i32, vp, vp, vp, vp, C.c_size_t, vp]
+    lib.flashhead_verify.restype = C.c_int
     return lib
 
 
@@ -187,6 +204,45 @@ def dtype_code(t) -> int:
     if t.dtype in (torch.bfloat16, torch.int16, torch.uint16):
         return FH_DTYPE_BF16
     raise TypeError(f"unsupported dtype {t.dtype}")
+
+
+def _matrix(t, what: str, rows=None, cols=None, dtypes=None, like=None):
+    """Checks a device matrix (unit stride along a row) and returns its
+    address and row stride in elements; (None, 0) for None.  `like`: a tensor
+    of the same call whose device it must share."""
+    if t is None:
+        return None, 0
+    if t.dim() != 2 or (rows is not None and t.shape[0] != rows) or \
+            (cols is not None and t.shape[1] != cols):
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected "
+                         f"({'rows' if rows is None else rows}, {'columns' if cols is None else cols})")
+    ld = t.stride(0)
+    if t.shape[1] > 1 and t.stride(1) != 1 or t.shape[0] > 1 and ld < t.shape[1]:
+        raise ValueError(f"{what}: strides {t.stride()}, rows must be contiguous and not overlap")
+    _on_device(t, what, dtypes, like)
+    return t.data_ptr(), ld
+
+
+def _vector(t, what: str, n: int, dtypes, like=None):
+    """Checks a contiguous device vector and returns its address; None for None."""
+    if t is None:
+        return None
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{what}: {n} contiguous values expected, got shape {tuple(t.shape)}")
+    _on_device(t, what, dtypes, like)
+    return t.data_ptr()
+
+
+def _on_device(t, what: str, dtypes, like) -> None:
+    if dtypes is not None and t.dtype not in dtypes:
+        raise TypeError(f"{what}: unsupported dtype {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{what}: a device tensor is expected, got one on {t.device}")
+    if like is not None:
+        if t.device != like.device:
+            raise ValueError(f"{what}: on {t.device}, other arguments on {like.device}")
+    elif t.device.index != _torch().cuda.current_device():
+        raise ValueError(f"{what}: on {t.device}, which is not the current device")
 
 
 def _debug(dbg: Optional[dict]):
@@ -324,6 +380,89 @@ def dense_head_static(E, H, B: int, mode: int, tau: float, seeds, out_tokens,
     _check(lib.dense_head_static(_ptr(E), v, d, dtype_code(E), lde, _ptr(H), B, mode,
                                  tau, _ptr(seeds), _ptr(out_tokens), _ptr(out_lse),
                                  _stream(stream)), "dense_head_static")
+
+
+def flashhead_rmsnorm(x, weight=None, *, residual=None, residual_out=None, y=None, y8=None,
+                      y_scale=None, eps: float = 1e-6, weight_offset: float = 0.0,
+                      stream=None) -> None:
+    """RMS norm of the rows of x (+ residual) into the given outputs: t = x +
+    residual, y in x's dtype, y8 (torch.float8_e4m3fn) with y_scale per 128
+    columns."""
+    torch = _torch()
+    kinds = (torch.float32, torch.bfloat16)
+    xp, ldx = _matrix(x, "x", dtypes=kinds)
+    rows, d = x.shape
+    same = (x.dtype,)
+    rp, ldr = _matrix(residual, "residual", rows, d, same, x)
+    wp = _vector(weight, "weight", d, same, x)
+    op, ldro = _matrix(residual_out, "residual_out", rows, d, same, x)
+    yp, ldy = _matrix(y, "y", rows, d, same, x)
+    qp, ldq = _matrix(y8, "y8", rows, d, (torch.float8_e4m3fn,), x)
+    sp, lds = _matrix(y_scale, "y_scale", rows, -(-d // FH_FP8_BLOCK), (torch.float32,), x)
+    _check(lib.flashhead_rmsnorm(xp, ldx, rp, ldr, wp, rows, d, dtype_code(x), eps,
+                                 weight_offset, op, ldro, yp, ldy, qp, ldq, sp, lds,
+                                 _stream(stream)), "flashhead_rmsnorm")
+
+
+def flashhead_quantize_fp8(E, E8, E_scale, stream=None) -> None:
+    """E in torch.float8_e4m3fn codes E8 with a scale per 128 x 128 block."""
+    torch = _torch()
+    ep, lde = _matrix(E, "E", dtypes=(torch.float32, torch.bfloat16))
+    v, d = E.shape
+    qp, ldq = _matrix(E8, "E8", v, d, (torch.float8_e4m3fn,), E)
+    sp, lds = _matrix(E_scale, "E_scale", -(-v // FH_FP8_BLOCK), -(-d // FH_FP8_BLOCK),
+                      (torch.float32,), E)
+    _check(lib.flashhead_quantize_fp8(ep, v, d, dtype_code(E), lde, qp, ldq, sp, lds,
+                                      _stream(stream)), "flashhead_quantize_fp8")
+
+
+def dense_logits_fp8(h8, h_scale, E8, E_scale, out, stream=None) -> None:
+    """out (rows x v, fp32 or bf16) = the logits of 8-bit h and E."""
+    torch = _torch()
+    f8, f32 = (torch.float8_e4m3fn,), (torch.float32,)
+    hp, ldh = _matrix(h8, "h8", dtypes=f8)
+    rows, d = h8.shape
+    g = -(-d // FH_FP8_BLOCK)
+    ep, lde = _matrix(E8, "E8", None, d, f8, h8)
+    v = E8.shape[0]
+    hs, lds = _matrix(h_scale, "h_scale", rows, g, f32, h8)
+    es, ldes = _matrix(E_scale, "E_scale", -(-v // FH_FP8_BLOCK), g, f32, h8)
+    op, ldo = _matrix(out, "out", rows, v, (torch.float32, torch.bfloat16), h8)
+    _check(lib.dense_logits_fp8(hp, ldh, hs, lds, rows, ep, lde, es, ldes, v, d, op,
+                                dtype_code(out), ldo, _stream(stream)), "dense_logits_fp8")
+
+
+def flashhead_verify_workspace_bytes(B: int, rows: int, v: int) -> int:
+    return int(lib.flashhead_verify_workspace_bytes(B, rows, v))
+
+
+def flashhead_verify(logits, row_start, draft_tokens, out_tokens, out_accepted, workspace, *,
+                     mode: int = FH_MODE_SAMPLE, tau: float = 1.0, draft_probs=None,
+                     u_accept=None, u_sample=None, out_logp=None, stream=None) -> None:
+    """Verification of drafted tokens against the target's logits (rows x v)
+    from given uniform numbers; row_start holds B + 1 offsets."""
+    torch = _torch()
+    i32, f32 = (torch.int32,), (torch.float32,)
+    lp, ldl = _matrix(logits, "logits", dtypes=(torch.float32, torch.bfloat16))
+    rows, v = logits.shape
+    B, n = row_start.numel() - 1, draft_tokens.numel()
+    if B < 0:
+        raise ValueError("row_start: at least one offset is expected")
+    rp = _vector(row_start, "row_start", B + 1, i32, logits)
+    dp = _vector(draft_tokens, "draft_tokens", n, i32, logits)
+    qp, ldq = _matrix(draft_probs, "draft_probs", n, v, f32, logits)
+    ap = _vector(u_accept, "u_accept", n, f32, logits)
+    up = _vector(u_sample, "u_sample", B, f32, logits)
+    tp, ldt = _matrix(out_tokens, "out_tokens", B, None, i32, logits)
+    m = out_tokens.shape[1]
+    op, ldo = _matrix(out_logp, "out_logp", B, m, f32, logits)
+    if B > 1 and (ldt != m or out_logp is not None and ldo != m):
+        raise ValueError("out_tokens and out_logp must be contiguous")
+    cp = _vector(out_accepted, "out_accepted", B, i32, logits)
+    wp = _vector(workspace, "workspace", workspace.numel(), (torch.uint8,), logits)
+    _check(lib.flashhead_verify(lp, rows, v, dtype_code(logits), ldl, rp, B, dp, n, qp, ldq, mode,
+                                tau, ap, up, m, tp, cp, op, wp, workspace.numel(),
+                                _stream(stream)), "flashhead_verify")
 
 
 def flashhead_kmeans(E, c: int, init, max_iter: int, out_c2t, out_centroids=None, *,

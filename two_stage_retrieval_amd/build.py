@@ -22,7 +22,7 @@ LIB_TRACE = os.path.join(PKG, "libflashhead_trace.so")
 SOURCES = ["fh_api.hip", "fh_stage1.hip", "fh_decode_b1_adapt.hip", "fh_rowdot.hip",
            "fh_select.hip",
            "fh_prepare.hip", "fh_batched.hip", "fh_mc.hip",
-           "fh_kmeans.hip", "fh_host.cpp"]
+           "fh_kmeans.hip", "fh_norm.hip", "fh_logits8.hip", "fh_verify.hip", "fh_host.cpp"]
 
 # Packed-fp32 instructions are disabled for all device code.  Leading scalar
 # kernel arguments (up to 8 dwords) are preloaded into scalar registers by

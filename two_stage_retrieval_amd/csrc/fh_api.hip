@@ -599,6 +599,24 @@ int dense_impl(const void* E, int64_t v, int32_t d, int32_t dtype, int64_t lde, 
                int32_t B, int32_t mode, float tau, const uint64_t* seeds, int32_t* out_tokens,
                float* out_lse, void* workspace, bool clear_counters, void* stream);
 
+// The workspace of flashhead_verify, laid out from `base` (null: only its
+// size in bytes is wanted).
+size_t verify_layout(VerifyArgs& a, int B, uint8_t* base) {
+  size_t at = 0;
+  auto take = [&](size_t n) {
+    uint8_t* p = base ? base + at : nullptr;
+    at += (n + 15) / 16 * 16;
+    return p;
+  };
+  const size_t parts = (size_t)a.rows * (size_t)a.nchunk, seqs = (size_t)B;
+  a.part_sum = reinterpret_cast<double*>(take(parts * sizeof(double)));
+  a.part_weight = reinterpret_cast<double*>(take(seqs * (size_t)a.nchunk * sizeof(double)));
+  a.state = reinterpret_cast<VerifyState*>(take(seqs * sizeof(VerifyState)));
+  a.part_top = reinterpret_cast<float*>(take(parts * sizeof(float)));
+  a.part_best = reinterpret_cast<int32_t*>(take(parts * sizeof(int32_t)));
+  return at;
+}
+
 // The workspace of dense_head_static: the layout of dense_head's workspace
 // for FH_DENSE_STATIC_MAX_BATCH rows, one copy per device, held until the
 // process ends.  Host code never uses this name as an address: each
@@ -850,6 +868,122 @@ int dense_head_static(const void* E, int64_t v, int32_t d, int32_t dtype, int64_
   if (st != FH_OK) return st;
   return dense_impl(E, v, d, dtype, lde, H, B, mode, tau, seeds, out_tokens, out_lse, ws, true,
                     stream);
+}
+
+int flashhead_rmsnorm(const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                      const void* weight, int64_t rows, int32_t d, int32_t dtype, float eps,
+                      float weight_offset, void* residual_out, int64_t ldro, void* y, int64_t ldy,
+                      uint8_t* y8, int64_t ldy8, float* y_scale, int64_t lds, void* stream) {
+  const int st = check_rmsnorm(x, ldx, residual, ldr, weight, rows, d, dtype, eps, weight_offset,
+                               residual_out, ldro, y, ldy, y8, ldy8, y_scale, lds);
+  if (st != FH_OK || rows == 0) return st;
+  const int es = esize_of(dtype);
+  RmsnormArgs a{};
+  a.x = static_cast<const uint8_t*>(x);
+  a.x_bytes = ldx * es;
+  a.r = static_cast<const uint8_t*>(residual);
+  a.r_bytes = ldr * es;
+  a.w = static_cast<const uint8_t*>(weight);
+  a.d = d;
+  a.units = d * es / 16;
+  a.eps = eps;
+  a.offset = weight_offset;
+  a.r_out = static_cast<uint8_t*>(residual_out);
+  a.ro_bytes = ldro * es;
+  a.y = static_cast<uint8_t*>(y);
+  a.y_bytes = ldy * es;
+  a.y8 = y8;
+  a.ldy8 = ldy8;
+  a.scale = y_scale;
+  a.lds = lds;
+  FH_TRY(launch_rmsnorm(a, dtype, rows, static_cast<hipStream_t>(stream)));
+  return FH_OK;
+}
+
+int flashhead_quantize_fp8(const void* E, int64_t v, int32_t d, int32_t dtype, int64_t lde,
+                           uint8_t* E8, int64_t lde8, float* E_scale, int64_t lds, void* stream) {
+  const int st = check_quantize_fp8(E, v, d, dtype, lde, E8, lde8, E_scale, lds);
+  if (st != FH_OK) return st;
+  QuantizeFp8Args a{};
+  a.E = static_cast<const uint8_t*>(E);
+  a.e_bytes = lde * esize_of(dtype);
+  a.v = v;
+  a.d = d;
+  a.codes = E8;
+  a.ldc = lde8;
+  a.scale = E_scale;
+  a.lds = lds;
+  FH_TRY(launch_quantize_fp8(a, dtype, static_cast<hipStream_t>(stream)));
+  return FH_OK;
+}
+
+int dense_logits_fp8(const uint8_t* h8, int64_t ldh, const float* h_scale, int64_t lds,
+                     int32_t rows, const uint8_t* E8, int64_t lde, const float* E_scale,
+                     int64_t ldes, int64_t v, int32_t d, void* out, int32_t out_dtype, int64_t ldo,
+                     void* stream) {
+  const int st = check_logits_fp8(h8, ldh, h_scale, lds, rows, E8, lde, E_scale, ldes, v, d, out,
+                                  out_dtype, ldo);
+  if (st != FH_OK || rows == 0) return st;
+  Logits8Args a{};
+  a.h8 = h8;
+  a.ldh = ldh;
+  a.h_scale = h_scale;
+  a.lds = lds;
+  a.rows = rows;
+  a.E8 = E8;
+  a.lde = lde;
+  a.E_scale = E_scale;
+  a.ldes = ldes;
+  a.v = v;
+  a.d = d;
+  a.out = out;
+  a.ldo = ldo;
+  FH_TRY(launch_logits8(a, out_dtype, static_cast<hipStream_t>(stream)));
+  return FH_OK;
+}
+
+size_t flashhead_verify_workspace_bytes(int32_t B, int64_t rows, int64_t v) {
+  if (B < 0 || rows < 0 || v < 1 || v > (int64_t)INT32_MAX) return 0;
+  VerifyArgs a{};
+  a.rows = rows;
+  a.v = v;
+  plan_verify(a);
+  return verify_layout(a, B, nullptr);
+}
+
+int flashhead_verify(const void* logits, int64_t rows, int64_t v, int32_t dtype, int64_t ldl,
+                     const int32_t* row_start, int32_t B, const int32_t* draft_tokens,
+                     int64_t n_drafts, const float* draft_probs, int64_t ldq, int32_t mode,
+                     float tau, const float* u_accept, const float* u_sample, int32_t max_tokens,
+                     int32_t* out_tokens, int32_t* out_accepted, float* out_logp, void* workspace,
+                     size_t workspace_bytes, void* stream) {
+  const int st = check_verify(logits, rows, v, dtype, ldl, row_start, B, draft_tokens, n_drafts,
+                              draft_probs, ldq, mode, tau, u_accept, u_sample, max_tokens,
+                              out_tokens, out_accepted, workspace);
+  if (st != FH_OK || B == 0) return st;
+  VerifyArgs a{};
+  a.logits = static_cast<const uint8_t*>(logits);
+  a.l_bytes = ldl * esize_of(dtype);
+  a.rows = rows;
+  a.v = v;
+  a.row_start = row_start;
+  a.draft_tokens = draft_tokens;
+  a.n_drafts = n_drafts;
+  a.q = draft_probs;
+  a.ldq = ldq;
+  a.sample = mode == FH_MODE_SAMPLE;
+  a.inv_tau = a.sample ? 1.0 / (double)tau : 1.0;
+  a.u_accept = u_accept;
+  a.u_sample = u_sample;
+  a.max_tokens = max_tokens;
+  a.out_tokens = out_tokens;
+  a.out_accepted = out_accepted;
+  a.out_logp = out_logp;
+  plan_verify(a);
+  if (verify_layout(a, B, static_cast<uint8_t*>(workspace)) > workspace_bytes)
+    return FH_ERR_INVALID_ARG;
+  FH_TRY(launch_verify(a, dtype, B, static_cast<hipStream_t>(stream)));
+  return FH_OK;
 }
 
 }  // extern "C"

@@ -124,4 +124,109 @@ void quantize_int4(const uint16_t* C, const double* shift, int c, int d,
   *groups_out = G;
 }
 
+namespace {
+
+// one launch holds fewer than 2^32 threads, 256 of them a workgroup
+constexpr int64_t kMaxGroups = ((int64_t)1 << 24) - 1;
+
+bool aligned(const void* p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
+
+// an optional matrix of `es`-byte elements whose rows start at multiples of 16 bytes
+int check_rows16(const void* p, int64_t ld, int64_t cols, int es, int64_t rows) {
+  if (!p) return FH_OK;
+  if (rows > 1 && ld < cols) return FH_ERR_INVALID_ARG;
+  if (!aligned16(p) || (rows > 1 && (ld * es) % 16)) return FH_ERR_UNSUPPORTED;
+  return FH_OK;
+}
+
+}  // namespace
+
+int check_rmsnorm(const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                  const void* weight, int64_t rows, int32_t d, int32_t dtype, float eps,
+                  float weight_offset, const void* residual_out, int64_t ldro, const void* y,
+                  int64_t ldy, const void* y8, int64_t ldy8, const void* y_scale, int64_t lds) {
+  if (rows < 0 || d < 1 || !isfinite(eps) || eps < 0.0f || !isfinite(weight_offset))
+    return FH_ERR_INVALID_ARG;
+  if (rows > 0 && !x) return FH_ERR_INVALID_ARG;
+  if (rows > 0 && !y && !y8 && !residual_out) return FH_ERR_INVALID_ARG;
+  if ((y8 != nullptr) != (y_scale != nullptr)) return FH_ERR_INVALID_ARG;
+  const int es = esize_of(dtype);
+  if (!es || d > FH_MAX_NORM_D || ((int64_t)d * es) % 16 || rows > kMaxGroups)
+    return FH_ERR_UNSUPPORTED;
+  if (weight && !aligned16(weight)) return FH_ERR_UNSUPPORTED;
+  int st = check_rows16(x, ldx, d, es, rows);
+  if (st == FH_OK) st = check_rows16(residual, ldr, d, es, rows);
+  if (st == FH_OK) st = check_rows16(residual_out, ldro, d, es, rows);
+  if (st == FH_OK) st = check_rows16(y, ldy, d, es, rows);
+  if (st != FH_OK) return st;
+  if (y8) {
+    const int n = 16 / es;  // codes a thread stores at once
+    if (rows > 1 && (ldy8 < d || lds < (d + 127) / 128)) return FH_ERR_INVALID_ARG;
+    if (!aligned(y8, (uintptr_t)n) || (rows > 1 && ldy8 % n) || !aligned(y_scale, 4))
+      return FH_ERR_UNSUPPORTED;
+  }
+  return FH_OK;
+}
+
+int check_quantize_fp8(const void* E, int64_t v, int32_t d, int32_t dtype, int64_t lde,
+                       const void* E8, int64_t lde8, const void* E_scale, int64_t lds) {
+  if (!E || !E8 || !E_scale || v < 1 || d < 1) return FH_ERR_INVALID_ARG;
+  const int es = esize_of(dtype);
+  if (!es || ((int64_t)d * es) % 16 || v > (int64_t)65535 * 128) return FH_ERR_UNSUPPORTED;
+  const int st = check_rows16(E, lde, d, es, v);
+  if (st != FH_OK) return st;
+  if (v > 1 && lde8 < d) return FH_ERR_INVALID_ARG;
+  if (v > 128 && lds < (d + 127) / 128) return FH_ERR_INVALID_ARG;
+  const int n = 16 / es;
+  if (!aligned(E8, (uintptr_t)n) || (v > 1 && lde8 % n) || !aligned(E_scale, 4))
+    return FH_ERR_UNSUPPORTED;
+  return FH_OK;
+}
+
+int check_logits_fp8(const void* h8, int64_t ldh, const void* h_scale, int64_t lds, int32_t rows,
+                     const void* E8, int64_t lde, const void* E_scale, int64_t ldes, int64_t v,
+                     int32_t d, const void* out, int32_t out_dtype, int64_t ldo) {
+  if (rows < 0 || v < 1 || d < 1 || !E8 || !E_scale) return FH_ERR_INVALID_ARG;
+  if (rows > 0 && (!h8 || !h_scale || !out)) return FH_ERR_INVALID_ARG;
+  if (v > (int64_t)INT32_MAX || rows > 65535 * 16) return FH_ERR_UNSUPPORTED;
+  const int es = esize_of(out_dtype);
+  if (!es || d % 16) return FH_ERR_UNSUPPORTED;
+  const int32_t groups = (d + 127) / 128;
+  if ((rows > 1 && lds < groups) || (v > 128 && ldes < groups)) return FH_ERR_INVALID_ARG;
+  int st = check_rows16(h8, ldh, d, 1, rows);
+  if (st == FH_OK) st = check_rows16(E8, lde, d, 1, v);
+  if (st == FH_OK) st = check_rows16(out, ldo, v, es, rows);
+  if (st != FH_OK) return st;
+  if (!aligned(h_scale, 4) || !aligned(E_scale, 4)) return FH_ERR_UNSUPPORTED;
+  return FH_OK;
+}
+
+int check_verify(const void* logits, int64_t rows, int64_t v, int32_t dtype, int64_t ldl,
+                 const void* row_start, int32_t B, const void* draft_tokens, int64_t n_drafts,
+                 const void* draft_probs, int64_t ldq, int32_t mode, float tau,
+                 const void* u_accept, const void* u_sample, int32_t max_tokens,
+                 const void* out_tokens, const void* out_accepted, const void* workspace) {
+  if (B < 0 || rows < 0 || v < 1 || n_drafts < 0 || max_tokens < 1) return FH_ERR_INVALID_ARG;
+  if (mode != FH_MODE_GREEDY && mode != FH_MODE_SAMPLE) return FH_ERR_INVALID_ARG;
+  const bool sample = mode == FH_MODE_SAMPLE;
+  if (sample && (!(tau > 0.0f) || !isfinite(tau))) return FH_ERR_INVALID_ARG;
+  if (B > 0) {
+    if (!row_start || !out_tokens || !out_accepted || !workspace) return FH_ERR_INVALID_ARG;
+    if (rows > 0 && !logits) return FH_ERR_INVALID_ARG;
+    if (n_drafts > 0 && (!draft_tokens || (sample && !u_accept))) return FH_ERR_INVALID_ARG;
+    if (sample && !u_sample) return FH_ERR_INVALID_ARG;
+  }
+  if (draft_probs && !sample) return FH_ERR_INVALID_ARG;
+  const int es = esize_of(dtype);
+  if (!es || v > (int64_t)INT32_MAX) return FH_ERR_UNSUPPORTED;
+  int st = check_rows16(logits, ldl, v, es, rows);
+  if (st == FH_OK) st = check_rows16(draft_probs, ldq, v, 4, n_drafts);
+  if (st != FH_OK) return st;
+  if (!aligned16(workspace)) return FH_ERR_UNSUPPORTED;
+  // a chunk has at least 2048 values
+  const int64_t chunks = (v + 2047) / 2048;
+  if (rows > kMaxGroups / chunks || B > kMaxGroups / chunks) return FH_ERR_UNSUPPORTED;
+  return FH_OK;
+}
+
 }  // namespace fh

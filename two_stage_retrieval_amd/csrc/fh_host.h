@@ -49,4 +49,22 @@ void quantize_int4(const uint16_t* C, const double* shift, int c, int d,
                    std::vector<uint8_t>& codes, std::vector<uint16_t>& scales, int* ntiles_out,
                    int* groups_out);
 
+// The argument checks of the calls around the 8-bit head (see
+// include/flashhead.h for what each call accepts): FH_OK, or the status the
+// call returns before it touches the device.
+int check_rmsnorm(const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                  const void* weight, int64_t rows, int32_t d, int32_t dtype, float eps,
+                  float weight_offset, const void* residual_out, int64_t ldro, const void* y,
+                  int64_t ldy, const void* y8, int64_t ldy8, const void* y_scale, int64_t lds);
+int check_quantize_fp8(const void* E, int64_t v, int32_t d, int32_t dtype, int64_t lde,
+                       const void* E8, int64_t lde8, const void* E_scale, int64_t lds);
+int check_logits_fp8(const void* h8, int64_t ldh, const void* h_scale, int64_t lds, int32_t rows,
+                     const void* E8, int64_t lde, const void* E_scale, int64_t ldes, int64_t v,
+                     int32_t d, const void* out, int32_t out_dtype, int64_t ldo);
+int check_verify(const void* logits, int64_t rows, int64_t v, int32_t dtype, int64_t ldl,
+                 const void* row_start, int32_t B, const void* draft_tokens, int64_t n_drafts,
+                 const void* draft_probs, int64_t ldq, int32_t mode, float tau,
+                 const void* u_accept, const void* u_sample, int32_t max_tokens,
+                 const void* out_tokens, const void* out_accepted, const void* workspace);
+
 }  // namespace fh

@@ -319,6 +319,96 @@ struct KMeansArgs {
   double* centroids;
 };
 hipError_t run_kmeans(const KMeansArgs& a, hipStream_t s, int* iters, int* status);
+
+// Norm and 8-bit quantization (fh_norm.hip).  Byte strides of rows end in
+// _bytes, strides in elements begin with ld.
+struct RmsnormArgs {
+  const uint8_t* x;
+  int64_t x_bytes;
+  const uint8_t* r;      // residual, or null
+  int64_t r_bytes;
+  const uint8_t* w;      // weight, or null (ones)
+  int d, units;          // columns; 16-byte chunks per row
+  float eps, offset;
+  uint8_t* r_out;        // x + r, or null
+  int64_t ro_bytes;
+  uint8_t* y;            // or null
+  int64_t y_bytes;
+  uint8_t* y8;           // e4m3 codes, or null
+  int64_t ldy8;
+  float* scale;          // rows x ceil(d / 128), with y8
+  int64_t lds;
+};
+hipError_t launch_rmsnorm(const RmsnormArgs& a, int dtype, int64_t rows, hipStream_t s);
+struct QuantizeFp8Args {
+  const uint8_t* E;
+  int64_t e_bytes;
+  int64_t v;
+  int d;
+  uint8_t* codes;
+  int64_t ldc;
+  float* scale;          // ceil(v / 128) x ceil(d / 128)
+  int64_t lds;
+};
+hipError_t launch_quantize_fp8(const QuantizeFp8Args& a, int dtype, hipStream_t s);
+
+// Logits of the 8-bit dense head (fh_logits8.hip).
+struct Logits8Args {
+  const uint8_t* h8;     // rows x d codes
+  int64_t ldh;
+  const float* h_scale;  // rows x ceil(d / 128)
+  int64_t lds;
+  int rows;
+  const uint8_t* E8;     // v x d codes
+  int64_t lde;
+  const float* E_scale;  // ceil(v / 128) x ceil(d / 128)
+  int64_t ldes;
+  int64_t v;
+  int d;
+  void* out;             // rows x v
+  int64_t ldo;
+};
+hipError_t launch_logits8(const Logits8Args& a, int out_dtype, hipStream_t s);
+
+// Verification of drafted tokens (fh_verify.hip).
+constexpr int kVerifyMaxUnits = 4;  // 8-value units per thread of a chunk
+enum VerifyKind : int { kVerifyDone = 0, kVerifyPlain = 1, kVerifyResidual = 2 };
+struct VerifyState {     // what the draw of a sequence needs
+  int kind;              // VerifyKind: nothing to draw, from p, from max(p - q, 0)
+  int at;                // accepted drafts
+  int64_t row, draft;    // the row that is drawn from, and its draft
+  float top;             // the row's maximum
+  double sum;            // and its sum of exp((z - top) / tau)
+};
+struct VerifyArgs {
+  const uint8_t* logits;
+  int64_t l_bytes;
+  int64_t rows, v;
+  const int32_t* row_start;  // B + 1
+  const int32_t* draft_tokens;
+  int64_t n_drafts;
+  const float* q;            // n_drafts x v probabilities, or null (one-hot)
+  int64_t ldq;
+  int sample;
+  double inv_tau;            // 1 / tau (1 for greedy decoding)
+  const float* u_accept;
+  const float* u_sample;
+  int max_tokens;
+  int32_t* out_tokens;       // B x max_tokens
+  int32_t* out_accepted;     // B
+  float* out_logp;           // B x max_tokens, or null
+  // workspace
+  int nchunk, units;         // chunks per row, 8-value units per thread of one
+  int64_t chunk;             // values per chunk
+  double* part_sum;          // rows x nchunk
+  double* part_weight;       // B x nchunk
+  VerifyState* state;        // B
+  float* part_top;           // rows x nchunk
+  int32_t* part_best;        // rows x nchunk
+};
+// chunk size for these sizes (units, chunk, nchunk of `a`)
+void plan_verify(VerifyArgs& a);
+hipError_t launch_verify(const VerifyArgs& a, int dtype, int B, hipStream_t s);
 hipError_t launch_cluster_major_copy(const uint8_t* E, int64_t lde_bytes, const int32_t* c2t,
                                      int64_t v, int64_t row_bytes, uint8_t* Ec, hipStream_t s);
 

@@ -1,0 +1,225 @@
+// The norm in front of the head and the 8-bit (e4m3) formats of the 8-bit
+// dense head:
+//  * rmsnorm: t = x + r, y = t / sqrt(mean(t^2) + eps) * (offset + w) per
+//    row, t and y rounded once to the storage type, and/or y in e4m3 with one
+//    fp32 scale per 128 columns;
+//  * quantize_fp8: a matrix in e4m3 with one fp32 scale per 128 x 128 block.
+// Scale of a block: max(max|y| / 448, 2^-126); code: e4m3 of y / scale, to
+// nearest, ties to even.  The floor keeps the scale a normal number, so that
+// y / scale stays exact enough for tiny blocks and a zero block divides by no
+// zero.
+#include "fh_device.h"
+#include "fh_internal.h"
+
+namespace fh {
+
+namespace {
+
+constexpr int kNormThreads = 256;
+constexpr float kE4m3Max = 448.0f;
+constexpr float kScaleFloor = 1.17549435e-38f;  // 2^-126
+
+// One 16-byte chunk of a row: 8 bf16 or 4 fp32 values.
+template <typename T> struct Unit;
+template <> struct Unit<bf16_t> {
+  static constexpr int kElems = 8;
+  __device__ __forceinline__ static void load(const uint8_t* p, float* v) {
+    const uint4 w = *reinterpret_cast<const uint4*>(p);
+    v[0] = bf16_lo(w.x); v[1] = bf16_hi(w.x); v[2] = bf16_lo(w.y); v[3] = bf16_hi(w.y);
+    v[4] = bf16_lo(w.z); v[5] = bf16_hi(w.z); v[6] = bf16_lo(w.w); v[7] = bf16_hi(w.w);
+  }
+  __device__ __forceinline__ static uint32_t pair(float a, float b) {
+    return (uint32_t)f32_to_bf16_rne(a) | ((uint32_t)f32_to_bf16_rne(b) << 16);
+  }
+  __device__ __forceinline__ static void store(uint8_t* p, const float* v) {
+    *reinterpret_cast<uint4*>(p) =
+        make_uint4(pair(v[0], v[1]), pair(v[2], v[3]), pair(v[4], v[5]), pair(v[6], v[7]));
+  }
+};
+template <> struct Unit<float> {
+  static constexpr int kElems = 4;
+  __device__ __forceinline__ static void load(const uint8_t* p, float* v) {
+    const float4 w = *reinterpret_cast<const float4*>(p);
+    v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w;
+  }
+  __device__ __forceinline__ static void store(uint8_t* p, const float* v) {
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  }
+};
+
+// four codes in one word (values within the format's range after the scale)
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
+}
+
+__device__ __forceinline__ float block_scale(float amax) {
+  return fmaxf(amax / kE4m3Max, kScaleFloor);
+}
+
+// largest value over the lanes of each aligned group of `lanes` (a power of two)
+template <int lanes>
+__device__ __forceinline__ float group_max(float x) {
+#pragma unroll
+  for (int o = 1; o < lanes; o <<= 1) x = fmaxf(x, __shfl_xor(x, o, kWave));
+  return x;
+}
+
+template <int n>
+__device__ __forceinline__ void store_codes(uint8_t* p, const float* q) {
+  if constexpr (n == 8)
+    *reinterpret_cast<uint2*>(p) =
+        make_uint2(e4m3x4(q[0], q[1], q[2], q[3]), e4m3x4(q[4], q[5], q[6], q[7]));
+  else
+    *reinterpret_cast<uint32_t*>(p) = e4m3x4(q[0], q[1], q[2], q[3]);
+}
+
+// One workgroup per row; the row stays in registers between the sum and the
+// outputs, so x may be y and r may be the residual's output.
+template <typename T, int kUnits>
+__global__ __launch_bounds__(kNormThreads) void rmsnorm_kernel(const RmsnormArgs a) {
+  constexpr int N = Unit<T>::kElems;
+  constexpr int kGroupLanes = 128 / N;  // lanes that hold one block of 128 columns
+  __shared__ float s_sum[kNormThreads / kWave];
+  const int64_t row = blockIdx.x;
+  const int tid = threadIdx.x;
+  const uint8_t* x = a.x + row * a.x_bytes;
+  float t[kUnits][N];
+  float ss = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) {
+    const int u = i * kNormThreads + tid;
+    if (u < a.units) {
+      Unit<T>::load(x + (int64_t)u * 16, t[i]);
+      if (a.r) {
+        float r[N];
+        Unit<T>::load(a.r + row * a.r_bytes + (int64_t)u * 16, r);
+#pragma unroll
+        for (int j = 0; j < N; ++j) t[i][j] += r[j];
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < N; ++j) t[i][j] = 0.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < N; ++j) ss = fmaf(t[i][j], t[i][j], ss);
+  }
+  ss = wave_sum(ss);
+  if ((tid & (kWave - 1)) == 0) s_sum[tid / kWave] = ss;
+  __syncthreads();
+  float tot = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kNormThreads / kWave; ++w) tot += s_sum[w];
+  const float rstd = 1.0f / sqrtf(tot / (float)a.d + a.eps);
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) {
+    const int u = i * kNormThreads + tid;
+    const bool in = u < a.units;
+    float y[N];
+    if (in) {
+      if (a.r_out) Unit<T>::store(a.r_out + row * a.ro_bytes + (int64_t)u * 16, t[i]);
+      float w[N];
+      if (a.w) Unit<T>::load(a.w + (int64_t)u * 16, w);
+#pragma unroll
+      for (int j = 0; j < N; ++j) y[j] = t[i][j] * rstd * ((a.w ? w[j] : 1.0f) + a.offset);
+      if (a.y) Unit<T>::store(a.y + row * a.y_bytes + (int64_t)u * 16, y);
+    } else {
+#pragma unroll
+      for (int j = 0; j < N; ++j) y[j] = 0.0f;
+    }
+    if (a.y8) {
+      float m = 0.0f;
+#pragma unroll
+      for (int j = 0; j < N; ++j) m = fmaxf(m, fabsf(y[j]));
+      const float s = block_scale(group_max<kGroupLanes>(m));
+      if (in) {
+        float q[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) q[j] = y[j] / s;
+        store_codes<N>(a.y8 + row * a.ldy8 + (int64_t)u * N, q);
+        if (u % kGroupLanes == 0) a.scale[row * a.lds + u / kGroupLanes] = s;
+      }
+    }
+  }
+}
+
+// One workgroup per 128 x 128 block, held in registers between the maximum
+// and the codes.
+template <typename T>
+__global__ __launch_bounds__(256) void quantize_fp8_kernel(const QuantizeFp8Args a) {
+  constexpr int N = Unit<T>::kElems;
+  constexpr int kLanes = 128 / N;         // lanes along a row of the block
+  constexpr int kRows = 256 / kLanes;     // rows per step
+  constexpr int kSteps = 128 / kRows;
+  __shared__ float s_max[256 / kWave];
+  const int tid = threadIdx.x;
+  const int64_t r0 = (int64_t)blockIdx.y * 128 + tid / kLanes;
+  const int col = blockIdx.x * 128 + (tid % kLanes) * N;
+  const bool cin = col < a.d;
+  float t[kSteps][N];
+  float m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) {
+    const int64_t r = r0 + i * kRows;
+    if (cin && r < a.v) {
+      Unit<T>::load(a.E + r * a.e_bytes + (int64_t)col * (16 / N), t[i]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < N; ++j) t[i][j] = 0.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < N; ++j) m = fmaxf(m, fabsf(t[i][j]));
+  }
+  m = wave_max(m);
+  if ((tid & (kWave - 1)) == 0) s_max[tid / kWave] = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 256 / kWave; ++w) m = fmaxf(m, s_max[w]);
+  const float s = block_scale(m);
+  if (tid == 0) a.scale[(int64_t)blockIdx.y * a.lds + blockIdx.x] = s;
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) {
+    const int64_t r = r0 + i * kRows;
+    if (cin && r < a.v) {
+      float q[N];
+#pragma unroll
+      for (int j = 0; j < N; ++j) q[j] = t[i][j] / s;
+      store_codes<N>(a.codes + r * a.ldc + col, q);
+    }
+  }
+}
+
+template <typename T>
+void enqueue_rmsnorm(const RmsnormArgs& a, int64_t rows, hipStream_t s) {
+  const dim3 grid((unsigned)rows), block(kNormThreads);
+  const int n = (a.units + kNormThreads - 1) / kNormThreads;
+  if (n <= 1)
+    hipLaunchKernelGGL((rmsnorm_kernel<T, 1>), grid, block, 0, s, a);
+  else if (n <= 2)
+    hipLaunchKernelGGL((rmsnorm_kernel<T, 2>), grid, block, 0, s, a);
+  else if (n <= 4)
+    hipLaunchKernelGGL((rmsnorm_kernel<T, 4>), grid, block, 0, s, a);
+  else
+    hipLaunchKernelGGL((rmsnorm_kernel<T, 8>), grid, block, 0, s, a);
+}
+
+}  // namespace
+
+hipError_t launch_rmsnorm(const RmsnormArgs& a, int dtype, int64_t rows, hipStream_t s) {
+  if (dtype == FH_DTYPE_BF16)
+    enqueue_rmsnorm<bf16_t>(a, rows, s);
+  else
+    enqueue_rmsnorm<float>(a, rows, s);
+  return hipGetLastError();
+}
+
+hipError_t launch_quantize_fp8(const QuantizeFp8Args& a, int dtype, hipStream_t s) {
+  const dim3 grid((unsigned)((a.d + 127) / 128), (unsigned)((a.v + 127) / 128));
+  if (dtype == FH_DTYPE_BF16)
+    hipLaunchKernelGGL(quantize_fp8_kernel<bf16_t>, grid, dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL(quantize_fp8_kernel<float>, grid, dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace fh
