@@ -121,6 +121,14 @@ def test_logits_one_nan_code_of_E(fh):
         assert torch.all(torch.isnan(out2[:, 77]))
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("rows,v,d", [(65, 65600, 144), (130, 65537, 256), (300, 40000, 1104),
+                                      (513, 33001, 384), (257, 65536, 16), (2100, 9000, 400)])
+def test_logits_many_tiles(fh, dtype, rows, v, d):
+    # enough tiles for the tiled kernels, cut in every direction
+    check(fh, rows, v, d, dtype, extra=16)
+
+
 def test_logits_no_rows(fh):
     h8, hs, E8, es = inputs(1, 64, 128)
     fh.dense_logits_fp8(h8[:0], hs[:0], E8, es, torch.empty(0, 64, device="cuda"))
@@ -154,7 +162,7 @@ def test_logits_outputs_past_32_bits(fh):
     fh.dense_logits_fp8(h8, hs, E8, es, out)
     torch.cuda.synchronize()
     assert rows * v > 2 ** 31
-    z, mag = ref.logits(h8[-3:], hs[-3:], E8[-1280:], es[-10:])
-    ref.check_logits(out[-3:, -1280:], z, mag, d)
-    z, mag = ref.logits(h8[:3], hs[:3], E8[:1280], es[:10])
-    ref.check_logits(out[:3, :1280], z, mag, d)
+    z, mag = ref.logits(h8[-70:], hs[-70:], E8[-1280:], es[-10:])
+    ref.check_logits(out[-70:, -1280:], z, mag, d)
+    z, mag = ref.logits(h8[:70], hs[:70], E8[:1280], es[:10])
+    ref.check_logits(out[:70, :1280], z, mag, d)

@@ -27,73 +27,391 @@ __device__ __forceinline__ v8bf to_bf16(int w0, int w1) {
   return v8bf{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-// D[i, j] = sum over 128 columns of A[i, :] . B[j, :], 16 x 16.  Lane l gives
-// 32 bytes of row l % 16 of A and of B (any order of the columns that both
-// share); it receives rows 4 (l / 16) + 0..3 of column l % 16.
+// A lane's 32 bytes of a 16-row operand's block, as the matrix instructions
+// take them: lane l gives bytes of row l % 16 (any order of the columns that
+// both operands share).
 //
-// The codes go through the bf16 instruction: the 8-bit one drops, within
-// small groups of products, the bits far below the group's largest product
-// (on codes spread over the format's range its sums were 4.5e-5 off, against
-// 3e-8 for the bf16 instruction).
-__device__ __forceinline__ v4f mfma128(v8i a, v8i b) {
+// kExact: as bf16 values, for the bf16 instruction.  Otherwise the codes, for
+// the 8-bit instruction, which runs at twice the rate but cuts products short:
+// within each group of 8 it drops the bits below 2^-13 of the group's largest
+// product (measured; 4.5e-5 of the result on codes spread over the whole
+// format, against 3e-8 for the bf16 instruction).  That is a fortieth of
+// what rounding a result to bf16 costs, so it serves bf16 outputs only, and
+// only where the rate of the matrix cores sets the time.
+template <bool kExact> struct Frag;
+template <> struct Frag<true> {
+  v8bf x[4];
+  __device__ __forceinline__ void set(v4i lo, v4i hi) {
+    x[0] = to_bf16(lo[0], lo[1]);
+    x[1] = to_bf16(lo[2], lo[3]);
+    x[2] = to_bf16(hi[0], hi[1]);
+    x[3] = to_bf16(hi[2], hi[3]);
+  }
+};
+template <> struct Frag<false> {
+  v8i x;
+  __device__ __forceinline__ void set(v4i lo, v4i hi) {
+    x = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  }
+};
+
+// D[i, j] = sum over a block's columns of A[i, :] . B[j, :]; lane l receives
+// rows 4 (l / 16) + 0..3 of column l % 16
+__device__ __forceinline__ v4f mfma128(const Frag<true>& a, const Frag<true>& b) {
   v4f c = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-  for (int i = 0; i < 8; i += 2)
-    c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(to_bf16(a[i], a[i + 1]), to_bf16(b[i], b[i + 1]),
-                                                c, 0, 0, 0);
+  for (int i = 0; i < 4; ++i)
+    c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.x[i], b.x[i], c, 0, 0, 0);
   return c;
 }
-
-// the 32 bytes of a row's block that lane quarter q gives: [16 q, 16 q + 16)
-// and the same 64 bytes on, zero past the row's end
-__device__ __forceinline__ v8i load_block(const uint8_t* row, int k, int d) {
-  v4i lo = {0, 0, 0, 0}, hi = {0, 0, 0, 0};
-  if (k < d) lo = *reinterpret_cast<const v4i*>(row + k);
-  if (k + 64 < d) hi = *reinterpret_cast<const v4i*>(row + k + 64);
-  return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+__device__ __forceinline__ v4f mfma128(const Frag<false>& a, const Frag<false>& b) {
+  const v4f zero = {0.0f, 0.0f, 0.0f, 0.0f};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a.x, b.x, zero, 0, 0, 0, 0, 0, 0);
 }
 
-// One wave per 16 rows of E and 16 rows of h.
-template <typename TO>
-__global__ __launch_bounds__(256) void logits8_kernel(const Logits8Args a) {
-  const int lane = threadIdx.x & 63, q = lane >> 4, c = lane & 15;
-  const int64_t n0 = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * 16;
-  const int m0 = blockIdx.y * 16;
-  if (n0 >= a.v) return;
-  const int64_t n = n0 + c < a.v ? n0 + c : a.v - 1;
-  const int m = m0 + c < a.rows ? m0 + c : a.rows - 1;
-  const uint8_t* e = a.E8 + n * a.lde;
-  const uint8_t* h = a.h8 + (int64_t)m * a.ldh;
-  const float* hs = a.h_scale + (int64_t)m * a.lds;
-  const float* es = a.E_scale + (n0 / 128) * a.ldes;
-  v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int k = 0; k < a.d; k += 128) {
-    const v4f p = mfma128(load_block(e, k + 16 * q, a.d), load_block(h, k + 16 * q, a.d));
-    const float s = hs[k / 128] * es[k / 128];
+// 16 bytes of a row at column k, zero past its end (d is a multiple of 16)
+__device__ __forceinline__ v4i chunk(const uint8_t* row, int k, int d) {
+  if (k < d) return *reinterpret_cast<const v4i*>(row + k);
+  return v4i{0, 0, 0, 0};
+}
+
+// The 4 NT results of a lane, columns n .. n + 4 NT of row m.
+template <typename TO, int NT>
+__device__ __forceinline__ void store_run(const Logits8Args& a, int m, int64_t n, const v4f* x) {
+  if constexpr (sizeof(TO) == 4) {
+    float* o = reinterpret_cast<float*>(a.out) + (int64_t)m * a.ldo + n;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i] = fmaf(p[i], s, acc[i]);
-  }
-  if (m0 + c >= a.rows) return;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t t = n0 + 4 * q + i;
-    if (t < a.v) {
-      if constexpr (sizeof(TO) == 4)
-        reinterpret_cast<float*>(a.out)[(int64_t)m * a.ldo + t] = acc[i];
+    for (int j = 0; j < NT; ++j) {
+      if (n + 4 * j + 4 <= a.v)
+        *reinterpret_cast<v4f*>(o + 4 * j) = x[j];
       else
-        reinterpret_cast<uint16_t*>(a.out)[(int64_t)m * a.ldo + t] = f32_to_bf16_rne(acc[i]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (n + 4 * j + i < a.v) o[4 * j + i] = x[j][i];
     }
+  } else {
+    uint16_t* o = reinterpret_cast<uint16_t*>(a.out) + (int64_t)m * a.ldo + n;
+    constexpr int P = NT > 1 ? 2 : 1;   // 8 or 4 values at a time
+#pragma unroll
+    for (int j = 0; j < NT; j += P) {
+      uint16_t y[4 * P];
+#pragma unroll
+      for (int i = 0; i < 4 * P; ++i) y[i] = f32_to_bf16_rne(x[j + i / 4][i % 4]);
+      if (n + 4 * (j + P) <= a.v) {
+        uint32_t u[2 * P];
+#pragma unroll
+        for (int i = 0; i < 2 * P; ++i) u[i] = (uint32_t)y[2 * i] | ((uint32_t)y[2 * i + 1] << 16);
+        if constexpr (P == 2)
+          *reinterpret_cast<uint4*>(o + 4 * j) = make_uint4(u[0], u[1], u[2], u[3]);
+        else
+          *reinterpret_cast<uint2*>(o + 4 * j) = make_uint2(u[0], u[1]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4 * P; ++i)
+          if (n + 4 * j + i < a.v) o[4 * j + i] = y[i];
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Tiles: kBM rows of h by 256 rows of E per workgroup of 8 waves, each wave
+// kBM / 2 by 64.  Blocks of 128 columns go from memory to LDS without
+// passing registers (two buffers: the next block's loads run under the
+// present block's products).
+// ---------------------------------------------------------------------------
+constexpr int kBN = 256;
+
+// LDS rows are 128 bytes: eight 16-byte slots.  Chunk k of row r is held in
+// slot k ^ key(r), so that the eight lanes that read one chunk of eight rows
+// at a time touch eight different slots.
+__device__ __forceinline__ int key_h(int r) { return r & 7; }
+// (a wave's tile j of E has the rows 16 (c / 4) + 4 j + c % 4, c = 0 .. 15)
+__device__ __forceinline__ int key_e(int r) { return (r & 3) | ((r >> 2) & 4); }
+
+typedef __attribute__((address_space(1))) const void* gptr_t;
+typedef __attribute__((address_space(3))) void* lptr_t;
+
+template <int kBM, bool kExact, typename TO>
+__global__ __launch_bounds__(512, 2) void logits8_tiles_kernel(const Logits8Args a) {
+  constexpr int MT = kBM / 32;   // 16-row tiles of h per wave
+  __shared__ __align__(128) uint8_t s_e[2][kBN * 128];
+  __shared__ __align__(128) uint8_t s_h[2][kBM * 128];
+  __shared__ __align__(128) float s_hs[2][kBM];
+  const int tid = threadIdx.x, lane = tid & 63, q = lane >> 4, c = lane & 15;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6), wm = w >> 2, wn = w & 3;
+
+  // Workgroups are dealt to the 8 compute dies in turn: give each die a run
+  // of tiles, up to 8 of h under one of E, so that a die reads its rows of E
+  // into its cache once.
+  const unsigned per = gridDim.x / 8;
+  const unsigned tile = (blockIdx.x % 8) * per + blockIdx.x / 8;
+  const unsigned mt = (unsigned)(a.rows + kBM - 1) / kBM, nt = (unsigned)((a.v + kBN - 1) / kBN);
+  if (tile >= mt * nt) return;
+  const unsigned group = tile / (8 * nt), gm = min(8u, mt - group * 8);
+  const unsigned in = tile - group * 8 * nt;
+  const int m0 = (int)(group * 8 + in % gm) * kBM;
+  const int64_t n0 = (int64_t)(in / gm) * kBN;
+
+  // loads: each wave fills 8 rows of 8 slots at a time
+  const int lr = lane >> 3, slot = lane & 7;
+  const uint8_t* e_base = a.E8 + n0 * a.lde;
+  const uint8_t* h_base = a.h8 + (int64_t)m0 * a.ldh;
+  const int e_last = (int)(a.v - 1 - n0), h_last = a.rows - 1 - m0;
+  const int e_k = 16 * (slot ^ key_e(w * 8 + lr)), h_k = 16 * (slot ^ key_h(lr));
+  uint32_t e_off[kBN / 64], h_off[kBM / 64];
+#pragma unroll
+  for (int i = 0; i < kBN / 64; ++i)
+    e_off[i] = (uint32_t)min(i * 64 + w * 8 + lr, e_last) * (uint32_t)a.lde;
+#pragma unroll
+  for (int i = 0; i < kBM / 64; ++i)
+    h_off[i] = (uint32_t)min(i * 64 + w * 8 + lr, h_last) * (uint32_t)a.ldh;
+  const float* hs_base = a.h_scale + (int64_t)m0 * a.lds;
+  const uint32_t hs_off = (uint32_t)min(tid, h_last) * (uint32_t)a.lds;
+  auto load = [&](int kb, int st) {
+    const int k0 = kb * 128;
+    // a chunk past the row's end: the row's first bytes instead, which the
+    // products leave out
+    const int ek = k0 + e_k < a.d ? e_k : -k0, hk = k0 + h_k < a.d ? h_k : -k0;
+    const uint8_t* eb = e_base + k0;
+    const uint8_t* hb = h_base + k0;
+#pragma unroll
+    for (int i = 0; i < kBN / 64; ++i)
+      __builtin_amdgcn_global_load_lds((gptr_t)(eb + (int64_t)(int32_t)(e_off[i] + ek)),
+                                       (lptr_t)(s_e[st] + (i * 64 + w * 8) * 128), 16, 0, 0);
+#pragma unroll
+    for (int i = 0; i < kBM / 64; ++i)
+      __builtin_amdgcn_global_load_lds((gptr_t)(hb + (int64_t)(int32_t)(h_off[i] + hk)),
+                                       (lptr_t)(s_h[st] + (i * 64 + w * 8) * 128), 16, 0, 0);
+    if (w < kBM / 64)
+      __builtin_amdgcn_global_load_lds((gptr_t)(hs_base + kb + hs_off),
+                                       (lptr_t)(s_hs[st] + w * 64), 4, 0, 0);
+  };
+
+  const int64_t eb = min((n0 + wn * 64) / 128, (a.v - 1) / 128);
+  const float* es = a.E_scale + eb * a.ldes;
+  v4f acc[MT][4];
+#pragma unroll
+  for (int t = 0; t < MT; ++t)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[t][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+
+  // where the lane's operands are in LDS: row and byte of the first chunk (the
+  // second is four slots on); tiles are 4 rows of E, 16 of h apart
+  const int e_row = wn * 64 + 16 * (c >> 2) + (c & 3), e_slot = 16 * (q ^ key_e(e_row));
+  const int h_row = wm * (kBM / 2) + c, h_slot = 16 * (q ^ key_h(c));
+  const int G = (a.d + 127) / 128;
+  // the last block of a row that is not whole: h counts as zero past its end
+  auto cut = [&](int st) {
+    const int from = (a.d % 128) / 16;
+    for (int i = tid; i < kBM * 8; i += 512)
+      if ((i & 7) >= from)
+        *reinterpret_cast<v4i*>(s_h[st] + (i >> 3) * 128 + 16 * ((i & 7) ^ key_h(i >> 3))) =
+            v4i{0, 0, 0, 0};
+    __syncthreads();
+  };
+  load(0, 0);
+  __syncthreads();
+  if (G == 1 && a.d % 128) cut(0);
+  for (int kb = 0; kb < G; ++kb) {
+    const int st = kb & 1;
+    if (kb + 1 < G) load(kb + 1, st ^ 1);
+    const float s_e_scale = es[kb];
+    Frag<kExact> e[4];
+    const uint8_t* pe = s_e[st] + e_row * 128;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      e[j].set(*reinterpret_cast<const v4i*>(pe + j * 512 + e_slot),
+               *reinterpret_cast<const v4i*>(pe + j * 512 + (e_slot ^ 64)));
+    const uint8_t* ph = s_h[st] + h_row * 128;
+    v4i lo, hi;
+    float s;
+    auto read_h = [&](int t) {
+      lo = *reinterpret_cast<const v4i*>(ph + t * 2048 + h_slot);
+      hi = *reinterpret_cast<const v4i*>(ph + t * 2048 + (h_slot ^ 64));
+      s = s_hs[st][h_row + t * 16];
+    };
+    read_h(0);
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      Frag<kExact> h;
+      h.set(lo, hi);
+      const float x_scale = s * s_e_scale;
+      if (t + 1 < MT) read_h(t + 1);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const v4f x = mfma128(e[j], h);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[t][j][i] = fmaf(x[i], x_scale, acc[t][j][i]);
+      }
+      // Reads stay one tile ahead, and a tile's sums are taken here: the
+      // compiler would otherwise gather all reads in front and all sums
+      // behind, which do not fit the registers.
+#pragma unroll
+      for (int j = 0; j < 4; ++j) asm volatile("" : "+v"(acc[t][j]));
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    __syncthreads();
+    if (kb + 2 == G && a.d % 128) cut(st ^ 1);
+  }
+#pragma unroll
+  for (int t = 0; t < MT; ++t) {
+    const int m = m0 + wm * (kBM / 2) + t * 16 + c;
+    if (m < a.rows)
+      store_run<TO, 4>(a, m, n0 + wn * 64 + q * 16, acc[t]);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Few rows, or few tiles: one wave per 16 MT rows of h and 64 rows of E, or
+// four waves that share such a tile's columns and add their sums through LDS.
+// Operands go straight to registers: each is used MT (or 4) times.
+// ---------------------------------------------------------------------------
+template <int MT, int NT, int kSplit, typename TO>
+__global__ __launch_bounds__(256) void logits8_rows_kernel(const Logits8Args a) {
+  const int lane = threadIdx.x & 63, q = lane >> 4, c = lane & 15;
+  const int w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int64_t n0 = ((int64_t)blockIdx.x * (kSplit == 1 ? 4 : 1) + (kSplit == 1 ? w : 0)) * (16 * NT);
+  const int m0 = blockIdx.y * (16 * MT);
+  if (kSplit == 1 && n0 >= a.v) return;
+  const uint8_t* e[NT];
+  const uint8_t* h[MT];
+  const float* hs[MT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    // (NT > 1: the rows of a lane's results are then neighbours, as in the tiles)
+    const int64_t n = n0 + (c >> 2) * (4 * NT) + 4 * j + (c & 3);
+    e[j] = a.E8 + (n < a.v ? n : a.v - 1) * a.lde;
+  }
+#pragma unroll
+  for (int t = 0; t < MT; ++t) {
+    const int m = m0 + 16 * t + c < a.rows ? m0 + 16 * t + c : a.rows - 1;
+    h[t] = a.h8 + (int64_t)m * a.ldh;
+    hs[t] = a.h_scale + (int64_t)m * a.lds;
+  }
+  const float* es = a.E_scale + (n0 / 128) * a.ldes;
+  v4f acc[MT][NT];
+#pragma unroll
+  for (int t = 0; t < MT; ++t)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[t][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  const int G = (a.d + 127) / 128;
+  // the next block's rows are on their way while this one is multiplied
+  struct Raw { v4i lo, hi; } re[NT], rh[MT];
+  float s[MT];
+  auto load = [&](int kb) {
+    const int k = kb * 128 + 16 * q;
+#pragma unroll
+    for (int j = 0; j < NT; ++j) re[j] = Raw{chunk(e[j], k, a.d), chunk(e[j], k + 64, a.d)};
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      rh[t] = Raw{chunk(h[t], k, a.d), chunk(h[t], k + 64, a.d)};
+      s[t] = hs[t][kb] * es[kb];
+    }
+  };
+  int kb = kSplit == 1 ? 0 : w;
+  if (kb < G) load(kb);
+  for (; kb < G; kb += kSplit) {
+    Frag<true> ef[NT], hf[MT];
+    float sc[MT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) ef[j].set(re[j].lo, re[j].hi);
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      hf[t].set(rh[t].lo, rh[t].hi);
+      sc[t] = s[t];
+    }
+    if (kb + kSplit < G) load(kb + kSplit);
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const v4f x = mfma128(ef[j], hf[t]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[t][j][i] = fmaf(x[i], sc[t], acc[t][j][i]);
+      }
+    }
+  }
+  if constexpr (kSplit > 1) {
+    // wave 0 adds the others' sums in wave order
+    __shared__ v4f s_acc[(kSplit - 1) * MT * NT * 64];
+    if (w > 0) {
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+          s_acc[(((w - 1) * MT + t) * NT + j) * 64 + lane] = acc[t][j];
+    }
+    __syncthreads();
+    if (w > 0) return;
+#pragma unroll
+    for (int u = 0; u < kSplit - 1; ++u)
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[t][j] += s_acc[((u * MT + t) * NT + j) * 64 + lane];
+  }
+#pragma unroll
+  for (int t = 0; t < MT; ++t) {
+    const int m = m0 + 16 * t + c;
+    if (m < a.rows) store_run<TO, NT>(a, m, n0 + q * (4 * NT), acc[t]);
+  }
+}
+
+template <int MT, typename TO>
+void enqueue_rows(const Logits8Args& a, bool split, hipStream_t s) {
+  const unsigned my = (unsigned)((a.rows + 16 * MT - 1) / (16 * MT));
+  const dim3 block(256);
+  if constexpr (MT == 1) {
+    if (!split) {
+      hipLaunchKernelGGL((logits8_rows_kernel<MT, 1, 1, TO>),
+                         dim3((unsigned)((a.v + 63) / 64), my), block, 0, s, a);
+      return;
+    }
+  }
+  if (split)
+    hipLaunchKernelGGL((logits8_rows_kernel<MT, 4, 4, TO>), dim3((unsigned)((a.v + 63) / 64), my),
+                       block, 0, s, a);
+  else
+    hipLaunchKernelGGL((logits8_rows_kernel<MT, 4, 1, TO>),
+                       dim3((unsigned)((a.v + 255) / 256), my), block, 0, s, a);
+}
+
+template <int kBM, bool kExact, typename TO>
+void enqueue_tiles(const Logits8Args& a, hipStream_t s) {
+  const int64_t tiles = (int64_t)((a.rows + kBM - 1) / kBM) * ((a.v + kBN - 1) / kBN);
+  hipLaunchKernelGGL((logits8_tiles_kernel<kBM, kExact, TO>), dim3((unsigned)((tiles + 7) / 8 * 8)),
+                     dim3(512), 0, s, a);
+}
+
+template <typename TO>
+void enqueue(const Logits8Args& a, hipStream_t s) {
+  constexpr bool exact = sizeof(TO) == 4;
+  const int64_t n256 = (a.v + 255) / 256;
+  if (!exact && a.rows > 128 && (int64_t)((a.rows + 255) / 256) * n256 >= 256) {
+    enqueue_tiles<256, false, TO>(a, s);
+  } else if (a.rows > 64 && (int64_t)((a.rows + 127) / 128) * n256 >= 256) {
+    enqueue_tiles<128, exact, TO>(a, s);
+  } else {
+    const bool split = a.v < 65536;
+    if (a.rows <= 16)
+      enqueue_rows<1, TO>(a, split, s);
+    else if (a.rows <= 32)
+      enqueue_rows<2, TO>(a, split, s);
+    else if (a.rows <= 48)
+      enqueue_rows<3, TO>(a, split, s);
+    else
+      enqueue_rows<4, TO>(a, split, s);
   }
 }
 
 }  // namespace
 
 hipError_t launch_logits8(const Logits8Args& a, int out_dtype, hipStream_t s) {
-  const dim3 grid((unsigned)((a.v + 63) / 64), (unsigned)((a.rows + 15) / 16));
   if (out_dtype == FH_DTYPE_BF16)
-    hipLaunchKernelGGL(logits8_kernel<uint16_t>, grid, dim3(256), 0, s, a);
+    enqueue<uint16_t>(a, s);
   else
-    hipLaunchKernelGGL(logits8_kernel<float>, grid, dim3(256), 0, s, a);
+    enqueue<float>(a, s);
   return hipGetLastError();
 }
 
