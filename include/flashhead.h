@@ -369,7 +369,8 @@ int flashhead_quantize_fp8(const void* E, int64_t v, int32_t d, int32_t dtype, i
  * fortieth of its rounding to bf16); fp32 outputs never do.
  *   h8, h_scale   device, rows x d and rows x ceil(d / 128)
  *   E8, E_scale   device, v x d and ceil(v / 128) x ceil(d / 128)
- *   d             a multiple of 16;  rows <= 65535 * 16
+ *   d             a multiple of 16;  rows <= 65535 * 16;  strides of h8,
+ *                 h_scale, E8 and E_scale below 2^22
  *   out           device, rows x v, FH_DTYPE_F32 or FH_DTYPE_BF16
  * Rows of h8, E8 and out start at multiples of 16 bytes (v itself may be any
  * size; columns [v, ldo) of out are left as they are).  A row's result does

@@ -76,7 +76,8 @@ def test_logits_refusals(fh):
         assert call(**kw) == inv, kw
     for kw in (dict(dtype=3), dict(d=248), dict(h=P + 8), dict(E=P + 4), dict(out=P + 8),
                dict(hs=P + 2), dict(es=P + 2), dict(ldh=264), dict(lde=264), dict(ldo=300),
-               dict(v=2 ** 31), dict(rows=65535 * 16 + 1)):
+               dict(v=2 ** 31, ldo=2 ** 31), dict(rows=65535 * 16 + 1), dict(ldh=1 << 22),
+               dict(lde=1 << 22), dict(lds=1 << 22), dict(ldes=1 << 22)):
         assert call(**kw) == uns, kw
 
 

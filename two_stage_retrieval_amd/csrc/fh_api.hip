@@ -925,15 +925,16 @@ int dense_logits_fp8(const uint8_t* h8, int64_t ldh, const float* h_scale, int64
                                   out_dtype, ldo);
   if (st != FH_OK || rows == 0) return st;
   Logits8Args a{};
+  // (strides that no second row uses may hold anything)
   a.h8 = h8;
-  a.ldh = ldh;
+  a.ldh = rows > 1 ? ldh : d;
   a.h_scale = h_scale;
-  a.lds = lds;
+  a.lds = rows > 1 ? lds : 0;
   a.rows = rows;
   a.E8 = E8;
-  a.lde = lde;
+  a.lde = v > 1 ? lde : d;
   a.E_scale = E_scale;
-  a.ldes = ldes;
+  a.ldes = v > 128 ? ldes : 0;
   a.v = v;
   a.d = d;
   a.out = out;

@@ -198,6 +198,11 @@ int check_logits_fp8(const void* h8, int64_t ldh, const void* h_scale, int64_t l
   if (st == FH_OK) st = check_rows16(out, ldo, v, es, rows);
   if (st != FH_OK) return st;
   if (!aligned(h_scale, 4) || !aligned(E_scale, 4)) return FH_ERR_UNSUPPORTED;
+  // a tile's 256 rows are reached by 32-bit offsets
+  const int64_t far = (int64_t)1 << 22;
+  if ((rows > 1 && (ldh >= far || lds >= far)) || (v > 1 && lde >= far) ||
+      (v > 128 && ldes >= far))
+    return FH_ERR_UNSUPPORTED;
   return FH_OK;
 }
 

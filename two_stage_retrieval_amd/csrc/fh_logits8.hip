@@ -75,41 +75,41 @@ __device__ __forceinline__ v4i chunk(const uint8_t* row, int k, int d) {
   return v4i{0, 0, 0, 0};
 }
 
-// The 4 NT results of a lane, columns n .. n + 4 NT of row m.
+// Column of result i (0 .. 3) of a lane's tile j in a run of 16 NT columns,
+// less i: each store instruction writes 64 bytes in a row (16 columns of
+// fp32, or of two tiles' 32 of bf16).  Result row r = 4 q + i of tile j is
+// row run_at(j, q) + i of E.
 template <typename TO, int NT>
-__device__ __forceinline__ void store_run(const Logits8Args& a, int m, int64_t n, const v4f* x) {
-  if constexpr (sizeof(TO) == 4) {
-    float* o = reinterpret_cast<float*>(a.out) + (int64_t)m * a.ldo + n;
+__device__ __forceinline__ int run_at(int j, int q) {
+  if constexpr (sizeof(TO) == 2 && NT > 1) return 32 * (j >> 1) + 8 * q + 4 * (j & 1);
+  return 16 * j + 4 * q;
+}
+
+// A lane's results of row m, columns n + run_at(j, q) + 0..3.
+template <typename TO, int NT>
+__device__ __forceinline__ void store_run(const Logits8Args& a, int m, int64_t n, int q,
+                                          const v4f* x) {
+  TO* row = reinterpret_cast<TO*>(a.out) + (int64_t)m * a.ldo;
+  constexpr int P = sizeof(TO) == 2 && NT > 1 ? 2 : 1;   // tiles per store
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      if (n + 4 * j + 4 <= a.v)
-        *reinterpret_cast<v4f*>(o + 4 * j) = x[j];
-      else
+  for (int j = 0; j < NT; j += P) {
+    const int64_t t = n + run_at<TO, NT>(j, q);
+    TO y[4 * P];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (n + 4 * j + i < a.v) o[4 * j + i] = x[j][i];
+    for (int i = 0; i < 4 * P; ++i) {
+      const float z = x[j + i / 4][i % 4];
+      if constexpr (sizeof(TO) == 4) y[i] = z;
+      else y[i] = __builtin_bit_cast(uint16_t, (__bf16)z);
     }
-  } else {
-    uint16_t* o = reinterpret_cast<uint16_t*>(a.out) + (int64_t)m * a.ldo + n;
-    constexpr int P = NT > 1 ? 2 : 1;   // 8 or 4 values at a time
+    if (t + 4 * P <= a.v) {
+      typedef uint32_t words __attribute__((ext_vector_type(P * sizeof(TO))));
+      words u;
+      __builtin_memcpy(&u, y, sizeof(u));
+      *reinterpret_cast<words*>(row + t) = u;
+    } else {
 #pragma unroll
-    for (int j = 0; j < NT; j += P) {
-      uint16_t y[4 * P];
-#pragma unroll
-      for (int i = 0; i < 4 * P; ++i) y[i] = f32_to_bf16_rne(x[j + i / 4][i % 4]);
-      if (n + 4 * (j + P) <= a.v) {
-        uint32_t u[2 * P];
-#pragma unroll
-        for (int i = 0; i < 2 * P; ++i) u[i] = (uint32_t)y[2 * i] | ((uint32_t)y[2 * i + 1] << 16);
-        if constexpr (P == 2)
-          *reinterpret_cast<uint4*>(o + 4 * j) = make_uint4(u[0], u[1], u[2], u[3]);
-        else
-          *reinterpret_cast<uint2*>(o + 4 * j) = make_uint2(u[0], u[1]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4 * P; ++i)
-          if (n + 4 * j + i < a.v) o[4 * j + i] = y[i];
-      }
+      for (int i = 0; i < 4 * P; ++i)
+        if (t + i < a.v) row[t + i] = y[i];
     }
   }
 }
@@ -126,11 +126,34 @@ constexpr int kBN = 256;
 // slot k ^ key(r), so that the eight lanes that read one chunk of eight rows
 // at a time touch eight different slots.
 __device__ __forceinline__ int key_h(int r) { return r & 7; }
-// (a wave's tile j of E has the rows 16 (c / 4) + 4 j + c % 4, c = 0 .. 15)
-__device__ __forceinline__ int key_e(int r) { return (r & 3) | ((r >> 2) & 4); }
+// (tiles of E take rows as run_at says: 8 lanes read rows of which bits 0, 1
+// and 3 differ, or 0 to 2)
+template <typename TO>
+__device__ __forceinline__ int key_e(int r) {
+  return sizeof(TO) == 2 ? (r & 3) | ((r >> 1) & 4) : r & 7;
+}
 
-typedef __attribute__((address_space(1))) const void* gptr_t;
-typedef __attribute__((address_space(3))) void* lptr_t;
+// Memory to LDS: 16 (or 4) bytes a lane from base + off to the wave's LDS
+// address, lane after lane.  Written as instructions because the compiler,
+// which cannot tell the two buffers apart, would wait for the next block's
+// loads before it reads the present one; the waits are load_lds_wait's.  They
+// write no register, so nothing can be taken for written too early.
+__device__ __forceinline__ uint32_t lds_address(void* p) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)p;
+}
+__device__ __forceinline__ void load_lds16(const void* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+               :
+               : "s"(lds), "v"(off), "s"(base)
+               : "memory", "m0");
+}
+__device__ __forceinline__ void load_lds4(const void* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
+               :
+               : "s"(lds), "v"(off), "s"(base)
+               : "memory", "m0");
+}
+__device__ __forceinline__ void load_lds_wait() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 template <int kBM, bool kExact, typename TO>
 __global__ __launch_bounds__(512, 2) void logits8_tiles_kernel(const Logits8Args a) {
@@ -138,6 +161,7 @@ __global__ __launch_bounds__(512, 2) void logits8_tiles_kernel(const Logits8Args
   __shared__ __align__(128) uint8_t s_e[2][kBN * 128];
   __shared__ __align__(128) uint8_t s_h[2][kBM * 128];
   __shared__ __align__(128) float s_hs[2][kBM];
+  __shared__ __align__(128) float s_es[2][kWave];  // the tile's two blocks of E, then copies
   const int tid = threadIdx.x, lane = tid & 63, q = lane >> 4, c = lane & 15;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6), wm = w >> 2, wn = w & 3;
 
@@ -158,7 +182,7 @@ __global__ __launch_bounds__(512, 2) void logits8_tiles_kernel(const Logits8Args
   const uint8_t* e_base = a.E8 + n0 * a.lde;
   const uint8_t* h_base = a.h8 + (int64_t)m0 * a.ldh;
   const int e_last = (int)(a.v - 1 - n0), h_last = a.rows - 1 - m0;
-  const int e_k = 16 * (slot ^ key_e(w * 8 + lr)), h_k = 16 * (slot ^ key_h(lr));
+  const int e_k = 16 * (slot ^ key_e<TO>(w * 8 + lr)), h_k = 16 * (slot ^ key_h(lr));
   uint32_t e_off[kBN / 64], h_off[kBM / 64];
 #pragma unroll
   for (int i = 0; i < kBN / 64; ++i)
@@ -166,30 +190,35 @@ __global__ __launch_bounds__(512, 2) void logits8_tiles_kernel(const Logits8Args
 #pragma unroll
   for (int i = 0; i < kBM / 64; ++i)
     h_off[i] = (uint32_t)min(i * 64 + w * 8 + lr, h_last) * (uint32_t)a.ldh;
+  // scales: wave w < kBM / 64 those of 64 rows of h, the last wave E's
   const float* hs_base = a.h_scale + (int64_t)m0 * a.lds;
-  const uint32_t hs_off = (uint32_t)min(tid, h_last) * (uint32_t)a.lds;
+  const float* es_base = a.E_scale + n0 / 128 * a.ldes;
+  const bool es_two = lane > 0 && n0 / 128 < (a.v - 1) / 128;
+  const uint32_t s_off = w == 7 ? (es_two ? (uint32_t)a.ldes * 4 : 0u)
+                                : (uint32_t)min(tid, h_last) * (uint32_t)a.lds * 4;
+  const uint32_t l_e = lds_address(s_e) + w * 1024, l_h = lds_address(s_h) + w * 1024;
+  const uint32_t l_s = w == 7 ? lds_address(s_es) : lds_address(s_hs) + w * 256;
   auto load = [&](int kb, int st) {
     const int k0 = kb * 128;
+    const bool whole = k0 + 128 <= a.d;
     // a chunk past the row's end: the row's first bytes instead, which the
     // products leave out
-    const int ek = k0 + e_k < a.d ? e_k : -k0, hk = k0 + h_k < a.d ? h_k : -k0;
-    const uint8_t* eb = e_base + k0;
-    const uint8_t* hb = h_base + k0;
+    const uint8_t* eb = whole ? e_base + k0 : e_base;
+    const uint8_t* hb = whole ? h_base + k0 : h_base;
+    const uint32_t ek = whole ? e_k : k0 + e_k < a.d ? k0 + e_k : 0;
+    const uint32_t hk = whole ? h_k : k0 + h_k < a.d ? k0 + h_k : 0;
 #pragma unroll
     for (int i = 0; i < kBN / 64; ++i)
-      __builtin_amdgcn_global_load_lds((gptr_t)(eb + (int64_t)(int32_t)(e_off[i] + ek)),
-                                       (lptr_t)(s_e[st] + (i * 64 + w * 8) * 128), 16, 0, 0);
+      load_lds16(eb, e_off[i] + ek, l_e + st * (kBN * 128) + i * 8192);
 #pragma unroll
     for (int i = 0; i < kBM / 64; ++i)
-      __builtin_amdgcn_global_load_lds((gptr_t)(hb + (int64_t)(int32_t)(h_off[i] + hk)),
-                                       (lptr_t)(s_h[st] + (i * 64 + w * 8) * 128), 16, 0, 0);
+      load_lds16(hb, h_off[i] + hk, l_h + st * (kBM * 128) + i * 8192);
     if (w < kBM / 64)
-      __builtin_amdgcn_global_load_lds((gptr_t)(hs_base + kb + hs_off),
-                                       (lptr_t)(s_hs[st] + w * 64), 4, 0, 0);
+      load_lds4(hs_base + kb, s_off, l_s + st * (kBM * 4));
+    else if (w == 7)
+      load_lds4(es_base + kb, s_off, l_s + st * (kWave * 4));
   };
 
-  const int64_t eb = min((n0 + wn * 64) / 128, (a.v - 1) / 128);
-  const float* es = a.E_scale + eb * a.ldes;
   v4f acc[MT][4];
 #pragma unroll
   for (int t = 0; t < MT; ++t)
@@ -197,8 +226,9 @@ __global__ __launch_bounds__(512, 2) void logits8_tiles_kernel(const Logits8Args
     for (int j = 0; j < 4; ++j) acc[t][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 
   // where the lane's operands are in LDS: row and byte of the first chunk (the
-  // second is four slots on); tiles are 4 rows of E, 16 of h apart
-  const int e_row = wn * 64 + 16 * (c >> 2) + (c & 3), e_slot = 16 * (q ^ key_e(e_row));
+  // second is four slots on), and the rows between tiles
+  const int e_row = wn * 64 + run_at<TO, 4>(0, c >> 2) + (c & 3);
+  const int e_slot = 16 * (q ^ key_e<TO>(e_row));
   const int h_row = wm * (kBM / 2) + c, h_slot = 16 * (q ^ key_h(c));
   const int G = (a.d + 127) / 128;
   // the last block of a row that is not whole: h counts as zero past its end
@@ -211,18 +241,19 @@ __global__ __launch_bounds__(512, 2) void logits8_tiles_kernel(const Logits8Args
     __syncthreads();
   };
   load(0, 0);
+  load_lds_wait();
   __syncthreads();
   if (G == 1 && a.d % 128) cut(0);
   for (int kb = 0; kb < G; ++kb) {
     const int st = kb & 1;
     if (kb + 1 < G) load(kb + 1, st ^ 1);
-    const float s_e_scale = es[kb];
+    const float s_e_scale = s_es[st][wn >> 1];
     Frag<kExact> e[4];
     const uint8_t* pe = s_e[st] + e_row * 128;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      e[j].set(*reinterpret_cast<const v4i*>(pe + j * 512 + e_slot),
-               *reinterpret_cast<const v4i*>(pe + j * 512 + (e_slot ^ 64)));
+      e[j].set(*reinterpret_cast<const v4i*>(pe + run_at<TO, 4>(j, 0) * 128 + e_slot),
+               *reinterpret_cast<const v4i*>(pe + run_at<TO, 4>(j, 0) * 128 + (e_slot ^ 64)));
     const uint8_t* ph = s_h[st] + h_row * 128;
     v4i lo, hi;
     float s;
@@ -231,6 +262,12 @@ __global__ __launch_bounds__(512, 2) void logits8_tiles_kernel(const Logits8Args
       hi = *reinterpret_cast<const v4i*>(ph + t * 2048 + (h_slot ^ 64));
       s = s_hs[st][h_row + t * 16];
     };
+    v4f x[4];
+    float xs = 0.0f;
+    auto add = [&](int t, int j) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[t][j][i] = fmaf(x[j][i], xs, acc[t][j][i]);
+    };
     read_h(0);
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
@@ -238,19 +275,37 @@ __global__ __launch_bounds__(512, 2) void logits8_tiles_kernel(const Logits8Args
       h.set(lo, hi);
       const float x_scale = s * s_e_scale;
       if (t + 1 < MT) read_h(t + 1);
+      // The products of this tile run while the last one's are added, one
+      // matrix instruction (32 cycles) to four sums (16).
+      v4f y[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const v4f x = mfma128(e[j], h);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[t][j][i] = fmaf(x[i], x_scale, acc[t][j][i]);
+        y[j] = mfma128(e[j], h);
+        if (t > 0) add(t - 1, j);
       }
-      // Reads stay one tile ahead, and a tile's sums are taken here: the
-      // compiler would otherwise gather all reads in front and all sums
-      // behind, which do not fit the registers.
 #pragma unroll
-      for (int j = 0; j < 4; ++j) asm volatile("" : "+v"(acc[t][j]));
+      for (int j = 0; j < 4; ++j) x[j] = y[j];
+      xs = x_scale;
+      if constexpr (!kExact) {
+        __builtin_amdgcn_sched_group_barrier(0x100, 3, 0);  // LDS reads
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // matrix instruction
+          __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);  // vector instructions
+        }
+      }
+      // (reads stay one tile ahead: all at once they would not fit the registers)
       __builtin_amdgcn_sched_barrier(0);
     }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) add(MT - 1, j);
+    // the sums are taken here: the compiler would gather them behind the
+    // loop's branch otherwise, and hold every product until then
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) asm volatile("" : "+v"(acc[t][j]));
+    load_lds_wait();
     __syncthreads();
     if (kb + 2 == G && a.d % 128) cut(st ^ 1);
   }
@@ -258,7 +313,7 @@ __global__ __launch_bounds__(512, 2) void logits8_tiles_kernel(const Logits8Args
   for (int t = 0; t < MT; ++t) {
     const int m = m0 + wm * (kBM / 2) + t * 16 + c;
     if (m < a.rows)
-      store_run<TO, 4>(a, m, n0 + wn * 64 + q * 16, acc[t]);
+      store_run<TO, 4>(a, m, n0 + wn * 64, q, acc[t]);
   }
 }
 
@@ -279,8 +334,7 @@ __global__ __launch_bounds__(256) void logits8_rows_kernel(const Logits8Args a) 
   const float* hs[MT];
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
-    // (NT > 1: the rows of a lane's results are then neighbours, as in the tiles)
-    const int64_t n = n0 + (c >> 2) * (4 * NT) + 4 * j + (c & 3);
+    const int64_t n = n0 + run_at<TO, NT>(j, c >> 2) + (c & 3);
     e[j] = a.E8 + (n < a.v ? n : a.v - 1) * a.lde;
   }
 #pragma unroll
@@ -354,7 +408,7 @@ __global__ __launch_bounds__(256) void logits8_rows_kernel(const Logits8Args a) 
 #pragma unroll
   for (int t = 0; t < MT; ++t) {
     const int m = m0 + 16 * t + c;
-    if (m < a.rows) store_run<TO, NT>(a, m, n0 + q * (4 * NT), acc[t]);
+    if (m < a.rows) store_run<TO, NT>(a, m, n0, q, acc[t]);
   }
 }
 
