@@ -13,6 +13,7 @@ namespace {
 
 typedef int v8i __attribute__((ext_vector_type(8)));
 typedef int v4i __attribute__((ext_vector_type(4)));
+typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 
 typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
@@ -153,11 +154,21 @@ __device__ __forceinline__ void load_lds4(const void* base, uint32_t off, uint32
                : "s"(lds), "v"(off), "s"(base)
                : "memory", "m0");
 }
-__device__ __forceinline__ void load_lds_wait() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// waits until at most n of the wave's later memory operations are open
+template <int n>
+__device__ __forceinline__ void load_lds_wait() {
+  asm volatile("s_waitcnt vmcnt(%0)" : : "i"(n) : "memory");
+}
+
+// One workgroup per compute unit takes tile after tile: a tile's first block is
+// loaded under the last products of the one before and waited for behind that
+// one's stores, which may still be on their way, so that neither stands alone.
+constexpr int kTileGroups = 256;  // compute units
 
 template <int kBM, bool kExact, typename TO>
 __global__ __launch_bounds__(512, 2) void logits8_tiles_kernel(const Logits8Args a) {
   constexpr int MT = kBM / 32;   // 16-row tiles of h per wave
+  constexpr int kStores = MT * (sizeof(TO) == 2 ? 2 : 4);   // of a wave's results
   __shared__ __align__(128) uint8_t s_e[2][kBN * 128];
   __shared__ __align__(128) uint8_t s_h[2][kBM * 128];
   __shared__ __align__(128) float s_hs[2][kBM];
@@ -165,39 +176,45 @@ __global__ __launch_bounds__(512, 2) void logits8_tiles_kernel(const Logits8Args
   const int tid = threadIdx.x, lane = tid & 63, q = lane >> 4, c = lane & 15;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6), wm = w >> 2, wn = w & 3;
 
-  // Workgroups are dealt to the 8 compute dies in turn: give each die a run
-  // of tiles, up to 8 of h under one of E, so that a die reads its rows of E
-  // into its cache once.
-  const unsigned per = gridDim.x / 8;
-  const unsigned tile = (blockIdx.x % 8) * per + blockIdx.x / 8;
+  // Workgroups are dealt to the 8 compute dies in turn: each die has a run of
+  // tiles, up to 8 of h under one of E, so that it reads its rows of E into
+  // its cache once.
   const unsigned mt = (unsigned)(a.rows + kBM - 1) / kBM, nt = (unsigned)((a.v + kBN - 1) / kBN);
-  if (tile >= mt * nt) return;
-  const unsigned group = tile / (8 * nt), gm = min(8u, mt - group * 8);
-  const unsigned in = tile - group * 8 * nt;
-  const int m0 = (int)(group * 8 + in % gm) * kBM;
-  const int64_t n0 = (int64_t)(in / gm) * kBN;
+  const unsigned tiles = mt * nt, per = (tiles + 7) / 8;
+  const unsigned last = min(tiles, (blockIdx.x % 8 + 1) * per);
+  unsigned tile = blockIdx.x % 8 * per + blockIdx.x / 8;
+  if (tile >= last) return;
 
-  // loads: each wave fills 8 rows of 8 slots at a time
+  // loads: each wave fills 8 rows of 8 slots at a time; scales: wave w < kBM /
+  // 64 those of 64 rows of h, the last wave E's
   const int lr = lane >> 3, slot = lane & 7;
-  const uint8_t* e_base = a.E8 + n0 * a.lde;
-  const uint8_t* h_base = a.h8 + (int64_t)m0 * a.ldh;
-  const int e_last = (int)(a.v - 1 - n0), h_last = a.rows - 1 - m0;
   const int e_k = 16 * (slot ^ key_e<TO>(w * 8 + lr)), h_k = 16 * (slot ^ key_h(lr));
-  uint32_t e_off[kBN / 64], h_off[kBM / 64];
-#pragma unroll
-  for (int i = 0; i < kBN / 64; ++i)
-    e_off[i] = (uint32_t)min(i * 64 + w * 8 + lr, e_last) * (uint32_t)a.lde;
-#pragma unroll
-  for (int i = 0; i < kBM / 64; ++i)
-    h_off[i] = (uint32_t)min(i * 64 + w * 8 + lr, h_last) * (uint32_t)a.ldh;
-  // scales: wave w < kBM / 64 those of 64 rows of h, the last wave E's
-  const float* hs_base = a.h_scale + (int64_t)m0 * a.lds;
-  const float* es_base = a.E_scale + n0 / 128 * a.ldes;
-  const bool es_two = lane > 0 && n0 / 128 < (a.v - 1) / 128;
-  const uint32_t s_off = w == 7 ? (es_two ? (uint32_t)a.ldes * 4 : 0u)
-                                : (uint32_t)min(tid, h_last) * (uint32_t)a.lds * 4;
   const uint32_t l_e = lds_address(s_e) + w * 1024, l_h = lds_address(s_h) + w * 1024;
   const uint32_t l_s = w == 7 ? lds_address(s_es) : lds_address(s_hs) + w * 256;
+  int m0;
+  int64_t n0;
+  const uint8_t *e_base, *h_base;
+  const float* s_base;
+  uint32_t e_off[kBN / 64], h_off[kBM / 64], s_off;
+  auto at = [&](unsigned tile) {
+    const unsigned group = tile / (8 * nt), gm = min(8u, mt - group * 8);
+    const unsigned in = tile - group * 8 * nt;
+    m0 = (int)(group * 8 + in % gm) * kBM;
+    n0 = (int64_t)(in / gm) * kBN;
+    e_base = a.E8 + n0 * a.lde;
+    h_base = a.h8 + (int64_t)m0 * a.ldh;
+    const int e_last = (int)min(a.v - 1 - n0, (int64_t)kBN), h_last = a.rows - 1 - m0;
+#pragma unroll
+    for (int i = 0; i < kBN / 64; ++i)
+      e_off[i] = (uint32_t)min(i * 64 + w * 8 + lr, e_last) * (uint32_t)a.lde;
+#pragma unroll
+    for (int i = 0; i < kBM / 64; ++i)
+      h_off[i] = (uint32_t)min(i * 64 + w * 8 + lr, h_last) * (uint32_t)a.ldh;
+    const bool two = lane > 0 && n0 / 128 < (a.v - 1) / 128;
+    s_base = w == 7 ? a.E_scale + n0 / 128 * a.ldes : a.h_scale + (int64_t)m0 * a.lds;
+    s_off = w == 7 ? (two ? (uint32_t)a.ldes * 4 : 0u)
+                   : (uint32_t)min(tid, h_last) * (uint32_t)a.lds * 4;
+  };
   auto load = [&](int kb, int st) {
     const int k0 = kb * 128;
     const bool whole = k0 + 128 <= a.d;
@@ -214,16 +231,10 @@ __global__ __launch_bounds__(512, 2) void logits8_tiles_kernel(const Logits8Args
     for (int i = 0; i < kBM / 64; ++i)
       load_lds16(hb, h_off[i] + hk, l_h + st * (kBM * 128) + i * 8192);
     if (w < kBM / 64)
-      load_lds4(hs_base + kb, s_off, l_s + st * (kBM * 4));
+      load_lds4(s_base + kb, s_off, l_s + st * (kBM * 4));
     else if (w == 7)
-      load_lds4(es_base + kb, s_off, l_s + st * (kWave * 4));
+      load_lds4(s_base + kb, s_off, l_s + st * (kWave * 4));
   };
-
-  v4f acc[MT][4];
-#pragma unroll
-  for (int t = 0; t < MT; ++t)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc[t][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 
   // where the lane's operands are in LDS: row and byte of the first chunk (the
   // second is four slots on), and the rows between tiles
@@ -240,13 +251,48 @@ __global__ __launch_bounds__(512, 2) void logits8_tiles_kernel(const Logits8Args
             v4i{0, 0, 0, 0};
     __syncthreads();
   };
-  load(0, 0);
-  load_lds_wait();
-  __syncthreads();
-  if (G == 1 && a.d % 128) cut(0);
-  for (int kb = 0; kb < G; ++kb) {
-    const int st = kb & 1;
-    if (kb + 1 < G) load(kb + 1, st ^ 1);
+
+  v4f acc[MT][4];
+  auto clear = [&]() {
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[t][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  };
+  // Stores the wave's part of the tile at m, n, which ends before the last
+  // column.  A row that does not exist goes to an offset past the resource's
+  // end, which drops the store: there are always kStores of them.
+  auto store = [&](int m, int64_t n) {
+    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(
+        static_cast<uint8_t*>(a.out) + ((int64_t)m * a.ldo + n) * sizeof(TO), 0, 0x7FFFFFFF,
+        0x00027000);
+    const uint32_t lane_off = (uint32_t)(c * a.ldo + run_at<TO, 4>(0, q)) * sizeof(TO);
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      const uint32_t off = m + t * 16 + c < a.rows
+                               ? lane_off + (uint32_t)(t * 16 * a.ldo) * sizeof(TO)
+                               : 0x80000000u;
+      if constexpr (sizeof(TO) == 2) {
+#pragma unroll
+        for (int j = 0; j < 4; j += 2) {
+          typedef __bf16 v4bf __attribute__((ext_vector_type(4)));
+          const v4bf l = __builtin_convertvector(acc[t][j], v4bf);
+          const v4bf h = __builtin_convertvector(acc[t][j + 1], v4bf);
+          const v8bf y = __builtin_shufflevector(l, h, 0, 1, 2, 3, 4, 5, 6, 7);
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u, y), rsrc,
+                                                 (int)(off + 32 * j), 0, 0);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u, acc[t][j]), rsrc,
+                                                 (int)(off + 64 * j), 0, 0);
+      }
+    }
+  };
+
+  // adds the products of the block in buffer st
+  auto block = [&](int st) {
     const float s_e_scale = s_es[st][wn >> 1];
     Frag<kExact> e[4];
     const uint8_t* pe = s_e[st] + e_row * 128;
@@ -300,20 +346,49 @@ __global__ __launch_bounds__(512, 2) void logits8_tiles_kernel(const Logits8Args
 #pragma unroll
     for (int j = 0; j < 4; ++j) add(MT - 1, j);
     // the sums are taken here: the compiler would gather them behind the
-    // loop's branch otherwise, and hold every product until then
+    // loop's branches otherwise, and hold every product until then
 #pragma unroll
     for (int t = 0; t < MT; ++t)
 #pragma unroll
       for (int j = 0; j < 4; ++j) asm volatile("" : "+v"(acc[t][j]));
-    load_lds_wait();
-    __syncthreads();
-    if (kb + 2 == G && a.d % 128) cut(st ^ 1);
-  }
+  };
+
+  at(tile);
+  load(0, 0);
+  load_lds_wait<0>();
+  __syncthreads();
+  if (G == 1 && a.d % 128) cut(0);
+  for (int st = 0; tile < last;) {
+    const int m1 = m0 + wm * (kBM / 2);
+    const int64_t n1 = n0 + wn * 64;
+    const bool inside = n0 + kBN <= a.v;
+    clear();
+    for (int kb = 0; kb + 1 < G; ++kb) {
+      load(kb + 1, st ^ 1);
+      block(st);
+      load_lds_wait<0>();
+      __syncthreads();
+      st ^= 1;
+      if (kb + 2 == G && a.d % 128) cut(st);
+    }
+    tile += kTileGroups / 8;
+    if (tile < last) {
+      at(tile);
+      load(0, st ^ 1);
+    }
+    block(st);
+    if (inside) {
+      store(m1, n1);
+      load_lds_wait<kStores>();
+    } else {  // the last column cuts some stores: value by value
 #pragma unroll
-  for (int t = 0; t < MT; ++t) {
-    const int m = m0 + wm * (kBM / 2) + t * 16 + c;
-    if (m < a.rows)
-      store_run<TO, 4>(a, m, n0 + wn * 64, q, acc[t]);
+      for (int t = 0; t < MT; ++t)
+        if (m1 + t * 16 + c < a.rows) store_run<TO, 4>(a, m1 + t * 16 + c, n1, q, acc[t]);
+      load_lds_wait<0>();
+    }
+    __syncthreads();
+    st ^= 1;
+    if (G == 1 && a.d % 128 && tile < last) cut(st);
   }
 }
 
@@ -433,15 +508,15 @@ void enqueue_rows(const Logits8Args& a, bool split, hipStream_t s) {
 
 template <int kBM, bool kExact, typename TO>
 void enqueue_tiles(const Logits8Args& a, hipStream_t s) {
-  const int64_t tiles = (int64_t)((a.rows + kBM - 1) / kBM) * ((a.v + kBN - 1) / kBN);
-  hipLaunchKernelGGL((logits8_tiles_kernel<kBM, kExact, TO>), dim3((unsigned)((tiles + 7) / 8 * 8)),
-                     dim3(512), 0, s, a);
+  hipLaunchKernelGGL((logits8_tiles_kernel<kBM, kExact, TO>), dim3(kTileGroups), dim3(512), 0, s,
+                     a);
 }
 
 template <typename TO>
 void enqueue(const Logits8Args& a, hipStream_t s) {
   constexpr bool exact = sizeof(TO) == 4;
-  const int64_t n256 = (a.v + 255) / 256;
+  // (the tiles reach 128 rows of out by 31-bit offsets)
+  const int64_t n256 = a.ldo * (int64_t)sizeof(TO) < 1 << 23 ? (a.v + 255) / 256 : 0;
   if (!exact && a.rows > 128 && (int64_t)((a.rows + 255) / 256) * n256 >= 256) {
     enqueue_tiles<256, false, TO>(a, s);
   } else if (a.rows > 64 && (int64_t)((a.rows + 127) / 128) * n256 >= 256) {
