@@ -160,9 +160,11 @@ __device__ __forceinline__ void load_lds_wait() {
   asm volatile("s_waitcnt vmcnt(%0)" : : "i"(n) : "memory");
 }
 
-// One workgroup per compute unit takes tile after tile: a tile's first block is
-// loaded under the last products of the one before and waited for behind that
-// one's stores, which may still be on their way, so that neither stands alone.
+// One workgroup per compute unit takes tile after tile.  The rows of E of block
+// s + 2 are requested during block s, as soon as every wave has its operands
+// of E in registers; those of h (which stay in the die's cache) one block
+// ahead.  This goes on over the ends of tiles, and a tile's stores are behind
+// the loads of the next one's first block, so that neither stands alone.
 constexpr int kTileGroups = 256;  // compute units
 
 template <int kBM, bool kExact, typename TO>
@@ -177,8 +179,8 @@ __global__ __launch_bounds__(512, 2) void logits8_tiles_kernel(const Logits8Args
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6), wm = w >> 2, wn = w & 3;
 
   // Workgroups are dealt to the 8 compute dies in turn: each die has a run of
-  // tiles, up to 8 of h under one of E, so that it reads its rows of E into
-  // its cache once.
+  // tiles, up to 4 of h under one of E, so that it reads its rows of E into
+  // its cache once for four tiles and keeps the rows of h there.
   const unsigned mt = (unsigned)(a.rows + kBM - 1) / kBM, nt = (unsigned)((a.v + kBN - 1) / kBN);
   const unsigned tiles = mt * nt, per = (tiles + 7) / 8;
   const unsigned last = min(tiles, (blockIdx.x % 8 + 1) * per);
@@ -191,22 +193,37 @@ __global__ __launch_bounds__(512, 2) void logits8_tiles_kernel(const Logits8Args
   const int e_k = 16 * (slot ^ key_e<TO>(w * 8 + lr)), h_k = 16 * (slot ^ key_h(lr));
   const uint32_t l_e = lds_address(s_e) + w * 1024, l_h = lds_address(s_h) + w * 1024;
   const uint32_t l_s = w == 7 ? lds_address(s_es) : lds_address(s_hs) + w * 256;
-  int m0;
-  int64_t n0;
+  auto place = [&](unsigned tile, int* m0, int64_t* n0) {
+    const unsigned group = tile / (4 * nt), gm = min(4u, mt - group * 4);
+    const unsigned in = tile - group * 4 * nt;
+    *m0 = (int)(group * 4 + in % gm) * kBM;
+    *n0 = (int64_t)(in / gm) * kBN;
+  };
+  // The two streams of loads: the tile and block that comes next, and where
+  // it is.  A chunk past a row's end: the row's first bytes instead, which the
+  // products leave out.
+  const int G = (a.d + 127) / 128;
+  unsigned e_tile = tile, h_tile = tile;
+  int e_kb = 0, h_kb = 0;
   const uint8_t *e_base, *h_base;
   const float* s_base;
   uint32_t e_off[kBN / 64], h_off[kBM / 64], s_off;
-  auto at = [&](unsigned tile) {
-    const unsigned group = tile / (8 * nt), gm = min(8u, mt - group * 8);
-    const unsigned in = tile - group * 8 * nt;
-    m0 = (int)(group * 8 + in % gm) * kBM;
-    n0 = (int64_t)(in / gm) * kBN;
+  auto e_at = [&]() {
+    int m0;
+    int64_t n0;
+    place(e_tile, &m0, &n0);
     e_base = a.E8 + n0 * a.lde;
-    h_base = a.h8 + (int64_t)m0 * a.ldh;
-    const int e_last = (int)min(a.v - 1 - n0, (int64_t)kBN), h_last = a.rows - 1 - m0;
+    const int e_last = (int)min(a.v - 1 - n0, (int64_t)kBN);
 #pragma unroll
     for (int i = 0; i < kBN / 64; ++i)
       e_off[i] = (uint32_t)min(i * 64 + w * 8 + lr, e_last) * (uint32_t)a.lde;
+  };
+  auto h_at = [&]() {
+    int m0;
+    int64_t n0;
+    place(h_tile, &m0, &n0);
+    h_base = a.h8 + (int64_t)m0 * a.ldh;
+    const int h_last = a.rows - 1 - m0;
 #pragma unroll
     for (int i = 0; i < kBM / 64; ++i)
       h_off[i] = (uint32_t)min(i * 64 + w * 8 + lr, h_last) * (uint32_t)a.ldh;
@@ -215,25 +232,42 @@ __global__ __launch_bounds__(512, 2) void logits8_tiles_kernel(const Logits8Args
     s_off = w == 7 ? (two ? (uint32_t)a.ldes * 4 : 0u)
                    : (uint32_t)min(tid, h_last) * (uint32_t)a.lds * 4;
   };
-  auto load = [&](int kb, int st) {
-    const int k0 = kb * 128;
+  // kELoads, kHLoads + 1 at most, of a wave; false when there is no more
+  constexpr int kELoads = kBN / 64;
+  auto load_e = [&](int st) {
+    if (e_tile >= last) return false;
+    const int k0 = e_kb * 128;
     const bool whole = k0 + 128 <= a.d;
-    // a chunk past the row's end: the row's first bytes instead, which the
-    // products leave out
-    const uint8_t* eb = whole ? e_base + k0 : e_base;
-    const uint8_t* hb = whole ? h_base + k0 : h_base;
-    const uint32_t ek = whole ? e_k : k0 + e_k < a.d ? k0 + e_k : 0;
-    const uint32_t hk = whole ? h_k : k0 + h_k < a.d ? k0 + h_k : 0;
+    const uint8_t* base = whole ? e_base + k0 : e_base;
+    const uint32_t k = whole ? e_k : k0 + e_k < a.d ? k0 + e_k : 0;
 #pragma unroll
-    for (int i = 0; i < kBN / 64; ++i)
-      load_lds16(eb, e_off[i] + ek, l_e + st * (kBN * 128) + i * 8192);
+    for (int i = 0; i < kELoads; ++i)
+      load_lds16(base, e_off[i] + k, l_e + st * (kBN * 128) + i * 8192);
+    if (++e_kb == G) {
+      e_kb = 0;
+      e_tile += kTileGroups / 8;
+      if (e_tile < last) e_at();
+    }
+    return true;
+  };
+  auto load_h = [&](int st) {
+    if (h_tile >= last) return;
+    const int k0 = h_kb * 128;
+    const bool whole = k0 + 128 <= a.d;
+    const uint8_t* base = whole ? h_base + k0 : h_base;
+    const uint32_t k = whole ? h_k : k0 + h_k < a.d ? k0 + h_k : 0;
 #pragma unroll
     for (int i = 0; i < kBM / 64; ++i)
-      load_lds16(hb, h_off[i] + hk, l_h + st * (kBM * 128) + i * 8192);
+      load_lds16(base, h_off[i] + k, l_h + st * (kBM * 128) + i * 8192);
     if (w < kBM / 64)
-      load_lds4(s_base + kb, s_off, l_s + st * (kBM * 4));
+      load_lds4(s_base + h_kb, s_off, l_s + st * (kBM * 4));
     else if (w == 7)
-      load_lds4(s_base + kb, s_off, l_s + st * (kWave * 4));
+      load_lds4(s_base + h_kb, s_off, l_s + st * (kWave * 4));
+    if (++h_kb == G) {
+      h_kb = 0;
+      h_tile += kTileGroups / 8;
+      if (h_tile < last) h_at();
+    }
   };
 
   // where the lane's operands are in LDS: row and byte of the first chunk (the
@@ -241,7 +275,6 @@ __global__ __launch_bounds__(512, 2) void logits8_tiles_kernel(const Logits8Args
   const int e_row = wn * 64 + run_at<TO, 4>(0, c >> 2) + (c & 3);
   const int e_slot = 16 * (q ^ key_e<TO>(e_row));
   const int h_row = wm * (kBM / 2) + c, h_slot = 16 * (q ^ key_h(c));
-  const int G = (a.d + 127) / 128;
   // the last block of a row that is not whole: h counts as zero past its end
   auto cut = [&](int st) {
     const int from = (a.d % 128) / 16;
@@ -266,23 +299,43 @@ __global__ __launch_bounds__(512, 2) void logits8_tiles_kernel(const Logits8Args
     const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(
         static_cast<uint8_t*>(a.out) + ((int64_t)m * a.ldo + n) * sizeof(TO), 0, 0x7FFFFFFF,
         0x00027000);
-    const uint32_t lane_off = (uint32_t)(c * a.ldo + run_at<TO, 4>(0, q)) * sizeof(TO);
+    if constexpr (sizeof(TO) == 2) {
+      // Eight rows of 128 bytes a store instead of sixteen of 64: lane c of a
+      // row's first 8 gives away its second half and takes lane c + 8's
+      // first (3 % of the whole at 2048 x 128256 x 2048).
+      const bool up = c >= 8;
+      const uint32_t lane_off = (uint32_t)((c & 7) * a.ldo + 8 * q + (up ? 32 : 0)) * 2;
 #pragma unroll
-    for (int t = 0; t < MT; ++t) {
-      const uint32_t off = m + t * 16 + c < a.rows
-                               ? lane_off + (uint32_t)(t * 16 * a.ldo) * sizeof(TO)
-                               : 0x80000000u;
-      if constexpr (sizeof(TO) == 2) {
+      for (int t = 0; t < MT; ++t) {
+        typedef __bf16 v4bf __attribute__((ext_vector_type(4)));
+        v4u y[2], z;
 #pragma unroll
-        for (int j = 0; j < 4; j += 2) {
-          typedef __bf16 v4bf __attribute__((ext_vector_type(4)));
-          const v4bf l = __builtin_convertvector(acc[t][j], v4bf);
-          const v4bf h = __builtin_convertvector(acc[t][j + 1], v4bf);
-          const v8bf y = __builtin_shufflevector(l, h, 0, 1, 2, 3, 4, 5, 6, 7);
-          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u, y), rsrc,
-                                                 (int)(off + 32 * j), 0, 0);
+        for (int j = 0; j < 4; j += 2)
+          y[j / 2] = __builtin_bit_cast(
+              v4u, __builtin_shufflevector(__builtin_convertvector(acc[t][j], v4bf),
+                                           __builtin_convertvector(acc[t][j + 1], v4bf), 0, 1, 2,
+                                           3, 4, 5, 6, 7));
+#pragma unroll
+        for (int i = 0; i < 4; ++i)  // row_ror:8: the lane 8 on in its row of 16
+          z[i] = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(up ? y[0][i] : y[1][i]), 0x128,
+                                                       0xf, 0xf, false);
+#pragma unroll
+        for (int o = 0; o < 2; ++o) {  // rows 0..7, then 8..15 of the 16
+          const v4u x = (o == 1) == up ? y[o] : z;
+          const uint32_t off =
+              m + t * 16 + o * 8 + (c & 7) < a.rows
+                  ? lane_off + (uint32_t)((t * 16 + o * 8) * a.ldo) * 2
+                  : 0x80000000u;
+          __builtin_amdgcn_raw_buffer_store_b128(x, rsrc, (int)off, 0, 0);
         }
-      } else {
+      }
+    } else {
+      const uint32_t lane_off = (uint32_t)(c * a.ldo + 4 * q) * 4;
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        const uint32_t off = m + t * 16 + c < a.rows
+                                 ? lane_off + (uint32_t)(t * 16 * a.ldo) * 4
+                                 : 0x80000000u;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u, acc[t][j]), rsrc,
@@ -291,8 +344,9 @@ __global__ __launch_bounds__(512, 2) void logits8_tiles_kernel(const Logits8Args
     }
   };
 
-  // adds the products of the block in buffer st
+  // adds the products of the block in buffer st; true if loads of E were made
   auto block = [&](int st) {
+    bool more = false;
     const float s_e_scale = s_es[st][wn >> 1];
     Frag<kExact> e[4];
     const uint8_t* pe = s_e[st] + e_row * 128;
@@ -307,6 +361,14 @@ __global__ __launch_bounds__(512, 2) void logits8_tiles_kernel(const Logits8Args
       lo = *reinterpret_cast<const v4i*>(ph + t * 2048 + h_slot);
       hi = *reinterpret_cast<const v4i*>(ph + t * 2048 + (h_slot ^ 64));
       s = s_hs[st][h_row + t * 16];
+    };
+    // The sums are taken here: the compiler would gather them behind the next
+    // branch otherwise, and hold every product until then.
+    auto pin = [&]() {
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) asm volatile("" : "+v"(acc[t][j]));
     };
     v4f x[4];
     float xs = 0.0f;
@@ -342,44 +404,51 @@ __global__ __launch_bounds__(512, 2) void logits8_tiles_kernel(const Logits8Args
       }
       // (reads stay one tile ahead: all at once they would not fit the registers)
       __builtin_amdgcn_sched_barrier(0);
+      if (t == 1) {  // E's operands are in every wave's registers
+        __builtin_amdgcn_s_barrier();
+        more = load_e(st);
+        pin();
+      }
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) add(MT - 1, j);
-    // the sums are taken here: the compiler would gather them behind the
-    // loop's branches otherwise, and hold every product until then
-#pragma unroll
-    for (int t = 0; t < MT; ++t)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) asm volatile("" : "+v"(acc[t][j]));
+    pin();
+    return more;
   };
 
-  at(tile);
-  load(0, 0);
+  e_at();
+  h_at();
+  load_e(0);
+  load_h(0);
+  load_e(1);
   load_lds_wait<0>();
   __syncthreads();
   if (G == 1 && a.d % 128) cut(0);
-  for (int st = 0; tile < last;) {
+  for (int st = 0; tile < last; tile += kTileGroups / 8) {
+    int m0;
+    int64_t n0;
+    place(tile, &m0, &n0);
     const int m1 = m0 + wm * (kBM / 2);
     const int64_t n1 = n0 + wn * 64;
-    const bool inside = n0 + kBN <= a.v;
     clear();
     for (int kb = 0; kb + 1 < G; ++kb) {
-      load(kb + 1, st ^ 1);
-      block(st);
-      load_lds_wait<0>();
+      load_h(st ^ 1);
+      if (block(st))
+        load_lds_wait<kELoads>();  // all but E's of the block after the next
+      else
+        load_lds_wait<0>();
       __syncthreads();
       st ^= 1;
       if (kb + 2 == G && a.d % 128) cut(st);
     }
-    tile += kTileGroups / 8;
-    if (tile < last) {
-      at(tile);
-      load(0, st ^ 1);
-    }
-    block(st);
-    if (inside) {
+    load_h(st ^ 1);
+    const bool more = block(st);
+    if (n0 + kBN <= a.v) {
       store(m1, n1);
-      load_lds_wait<kStores>();
+      if (more)
+        load_lds_wait<kELoads + kStores>();
+      else
+        load_lds_wait<kStores>();
     } else {  // the last column cuts some stores: value by value
 #pragma unroll
       for (int t = 0; t < MT; ++t)
@@ -388,7 +457,7 @@ __global__ __launch_bounds__(512, 2) void logits8_tiles_kernel(const Logits8Args
     }
     __syncthreads();
     st ^= 1;
-    if (G == 1 && a.d % 128 && tile < last) cut(st);
+    if (G == 1 && a.d % 128 && tile + kTileGroups / 8 < last) cut(st);
   }
 }
 
