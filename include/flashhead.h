@@ -363,8 +363,8 @@ int flashhead_quantize_fp8(const void* E, int64_t v, int32_t d, int32_t dtype, i
  *   out[m, t] = sum over k of h8[m, k] h_scale[m, k / 128]
  *                             * E8[t, k] E_scale[t / 128, k / 128]
  * with fp32 sums, rounded once to out_dtype.  Codes of the e4m3 NaN make the
- * outputs of their row NaN.  With bf16 outputs and many rows the products go
- * through the 8-bit matrix instruction, which drops the bits below 2^-13 of
+ * outputs of their row NaN.  With bf16 outputs and more than 16 rows the products
+ * may go through the 8-bit matrix instruction, which drops the bits below 2^-13 of
  * the largest product in each 8 columns (about 5e-5 of a typical result, a
  * fortieth of its rounding to bf16); fp32 outputs never do.
  *   h8, h_scale   device, rows x d and rows x ceil(d / 128)

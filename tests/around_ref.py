@@ -94,13 +94,13 @@ def check_logits(out, z, mag, d):
     not stated, so a whole step each); then the scales' product, its product
     with the sum and one addition per block, half a step each.
 
-    More than 64 rows with bf16 outputs may take the 8-bit matrix instruction,
+    More than 16 rows with bf16 outputs may take the 8-bit matrix instruction,
     which drops the bits below 2^-13 of the largest product of each 8: the 7
     others lose less than 7 * 2^-13 of it, and the groups' largest products
     sum to no more than all magnitudes."""
     g = -(-d // BLOCK)
     e = (128 * 2 + 2 + g) * U32 * 1.001
-    if out.dtype == torch.bfloat16 and out.shape[0] > 64:
+    if out.dtype == torch.bfloat16 and out.shape[0] > 16:
         e += 7 * 2.0 ** -13
     assert np.all(np.abs(f64(out) - z) <= e * mag + half_step(out.dtype) * (1.001 * np.abs(z)
                   + e * mag) + 2.0 ** -133)

@@ -4,6 +4,8 @@
 // 128 x 128 block of E.  The products of a block of 128 columns are summed by
 // the matrix cores; its fp32 result is then scaled and added to the fp32
 // accumulator, since the scales change from block to block.
+#include <math.h>
+
 #include "fh_device.h"
 #include "fh_internal.h"
 
@@ -38,7 +40,8 @@ __device__ __forceinline__ v8bf to_bf16(int w0, int w1) {
 // product (measured; 4.5e-5 of the result on codes spread over the whole
 // format, against 3e-8 for the bf16 instruction).  That is a fortieth of
 // what rounding a result to bf16 costs, so it serves bf16 outputs only, and
-// only where the rate of the matrix cores sets the time.
+// only from 17 rows of h on, where it is faster (32 x 128256 x 2048: 41 us, 51
+// with the bf16 instruction).
 template <bool kExact> struct Frag;
 template <> struct Frag<true> {
   v8bf x[4];
@@ -404,7 +407,7 @@ __global__ __launch_bounds__(512, 2) void logits8_tiles_kernel(const Logits8Args
       }
       // (reads stay one tile ahead: all at once they would not fit the registers)
       __builtin_amdgcn_sched_barrier(0);
-      if (t == 1) {  // E's operands are in every wave's registers
+      if (t == (MT > 2 ? 1 : 0)) {  // E's operands are in every wave's registers
         __builtin_amdgcn_s_barrier();
         more = load_e(st);
         pin();
@@ -462,17 +465,19 @@ __global__ __launch_bounds__(512, 2) void logits8_tiles_kernel(const Logits8Args
 }
 
 // ---------------------------------------------------------------------------
-// Few rows, or few tiles: one wave per 16 MT rows of h and 64 rows of E, or
-// four waves that share such a tile's columns and add their sums through LDS.
-// Operands go straight to registers: each is used MT (or 4) times.
+// Few rows, or few tiles: four waves share 16 MT rows of h and 16 NT of E,
+// take every fourth block of columns each, and add their sums through LDS in
+// wave order.  Operands go straight to registers, the next block's while the
+// present one is multiplied.
 // ---------------------------------------------------------------------------
-template <int MT, int NT, int kSplit, typename TO>
-__global__ __launch_bounds__(256) void logits8_rows_kernel(const Logits8Args a) {
+constexpr int kSplit = 4;
+
+template <int MT, int NT, typename TO>
+__global__ __launch_bounds__(256, 2) void logits8_rows_kernel(const Logits8Args a) {
   const int lane = threadIdx.x & 63, q = lane >> 4, c = lane & 15;
   const int w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int64_t n0 = ((int64_t)blockIdx.x * (kSplit == 1 ? 4 : 1) + (kSplit == 1 ? w : 0)) * (16 * NT);
+  const int64_t n0 = (int64_t)blockIdx.x * (16 * NT);
   const int m0 = blockIdx.y * (16 * MT);
-  if (kSplit == 1 && n0 >= a.v) return;
   const uint8_t* e[NT];
   const uint8_t* h[MT];
   const float* hs[MT];
@@ -507,7 +512,7 @@ __global__ __launch_bounds__(256) void logits8_rows_kernel(const Logits8Args a) 
       s[t] = hs[t][kb] * es[kb];
     }
   };
-  int kb = kSplit == 1 ? 0 : w;
+  int kb = w;
   if (kb < G) load(kb);
   for (; kb < G; kb += kSplit) {
     Frag<true> ef[NT], hf[MT];
@@ -530,25 +535,21 @@ __global__ __launch_bounds__(256) void logits8_rows_kernel(const Logits8Args a) 
       }
     }
   }
-  if constexpr (kSplit > 1) {
-    // wave 0 adds the others' sums in wave order
-    __shared__ v4f s_acc[(kSplit - 1) * MT * NT * 64];
-    if (w > 0) {
+  __shared__ v4f s_acc[(kSplit - 1) * MT * NT * 64];
+  if (w > 0) {
 #pragma unroll
-      for (int t = 0; t < MT; ++t)
+    for (int t = 0; t < MT; ++t)
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
-          s_acc[(((w - 1) * MT + t) * NT + j) * 64 + lane] = acc[t][j];
-    }
-    __syncthreads();
-    if (w > 0) return;
-#pragma unroll
-    for (int u = 0; u < kSplit - 1; ++u)
-#pragma unroll
-      for (int t = 0; t < MT; ++t)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) acc[t][j] += s_acc[((u * MT + t) * NT + j) * 64 + lane];
+      for (int j = 0; j < NT; ++j) s_acc[(((w - 1) * MT + t) * NT + j) * 64 + lane] = acc[t][j];
   }
+  __syncthreads();
+  if (w > 0) return;
+#pragma unroll
+  for (int u = 0; u < kSplit - 1; ++u)
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) acc[t][j] += s_acc[((u * MT + t) * NT + j) * 64 + lane];
 #pragma unroll
   for (int t = 0; t < MT; ++t) {
     const int m = m0 + 16 * t + c;
@@ -556,23 +557,12 @@ __global__ __launch_bounds__(256) void logits8_rows_kernel(const Logits8Args a) 
   }
 }
 
-template <int MT, typename TO>
-void enqueue_rows(const Logits8Args& a, bool split, hipStream_t s) {
-  const unsigned my = (unsigned)((a.rows + 16 * MT - 1) / (16 * MT));
-  const dim3 block(256);
-  if constexpr (MT == 1) {
-    if (!split) {
-      hipLaunchKernelGGL((logits8_rows_kernel<MT, 1, 1, TO>),
-                         dim3((unsigned)((a.v + 63) / 64), my), block, 0, s, a);
-      return;
-    }
-  }
-  if (split)
-    hipLaunchKernelGGL((logits8_rows_kernel<MT, 4, 4, TO>), dim3((unsigned)((a.v + 63) / 64), my),
-                       block, 0, s, a);
-  else
-    hipLaunchKernelGGL((logits8_rows_kernel<MT, 4, 1, TO>),
-                       dim3((unsigned)((a.v + 255) / 256), my), block, 0, s, a);
+template <int MT, int NT, typename TO>
+void enqueue_rows(const Logits8Args& a, hipStream_t s) {
+  hipLaunchKernelGGL((logits8_rows_kernel<MT, NT, TO>),
+                     dim3((unsigned)((a.v + 16 * NT - 1) / (16 * NT)),
+                          (unsigned)((a.rows + 16 * MT - 1) / (16 * MT))),
+                     dim3(256), 0, s, a);
 }
 
 template <int kBM, bool kExact, typename TO>
@@ -581,26 +571,49 @@ void enqueue_tiles(const Logits8Args& a, hipStream_t s) {
                      a);
 }
 
+// Time of a kernel in us: rounds of workgroups, blocks a workgroup walks, and
+// the measured time of a block (tiles: 64, 128, 256 rows of h with the 8-bit
+// instruction 0.8, 1.15, 2.2 us, 64 and 128 rows with the bf16 one 1.3 and
+// 2.4; four waves with 32 rows and 64 of E, two workgroups a compute unit: 3
+// us for four blocks).
+double rounds(int64_t groups, int at_once) { return (double)((groups + at_once - 1) / at_once); }
+template <typename TO>
+double tiles_time(const Logits8Args& a, int bm, double block) {
+  // (the tiles reach 128 rows of out by 31-bit offsets)
+  if (a.ldo * (int64_t)sizeof(TO) >= 1 << 23) return HUGE_VAL;
+  const int64_t tiles = (int64_t)((a.rows + bm - 1) / bm) * ((a.v + kBN - 1) / kBN);
+  return 2.0 + rounds(tiles, kTileGroups) * ((a.d + 127) / 128) * block;
+}
+
 template <typename TO>
 void enqueue(const Logits8Args& a, hipStream_t s) {
   constexpr bool exact = sizeof(TO) == 4;
-  // (the tiles reach 128 rows of out by 31-bit offsets)
-  const int64_t n256 = a.ldo * (int64_t)sizeof(TO) < 1 << 23 ? (a.v + 255) / 256 : 0;
-  if (!exact && a.rows > 128 && (int64_t)((a.rows + 255) / 256) * n256 >= 256) {
-    enqueue_tiles<256, false, TO>(a, s);
-  } else if (a.rows > 64 && (int64_t)((a.rows + 127) / 128) * n256 >= 256) {
-    enqueue_tiles<128, exact, TO>(a, s);
-  } else {
-    const bool split = a.v < 65536;
-    if (a.rows <= 16)
-      enqueue_rows<1, TO>(a, split, s);
-    else if (a.rows <= 32)
-      enqueue_rows<2, TO>(a, split, s);
-    else if (a.rows <= 48)
-      enqueue_rows<3, TO>(a, split, s);
+  if (a.rows <= 16) {
+    // As many rows of E a workgroup as leave most compute units one (1 x 4000
+    // x 4096: 7 us with 16, 9 with 32; 16 x 32000 x 2048: 14 us with 64, 21
+    // with 16); one row of h gains nothing from more than 32.
+    if (a.v > 64 * 192 && a.rows > 4)
+      enqueue_rows<1, 4, TO>(a, s);
+    else if (a.v > 32 * 192)
+      enqueue_rows<1, 2, TO>(a, s);
     else
-      enqueue_rows<4, TO>(a, split, s);
+      enqueue_rows<1, 1, TO>(a, s);
+    return;
   }
+  const double few = rounds((int64_t)((a.rows + 31) / 32) * ((a.v + 63) / 64), 2 * kTileGroups) *
+                     (((a.d + 127) / 128 + kSplit - 1) / kSplit) * 3.0;
+  const double t64 = tiles_time<TO>(a, 64, exact ? 1.3 : 0.8);
+  const double t128 = tiles_time<TO>(a, 128, exact ? 2.4 : 1.15);
+  const double t256 = exact ? HUGE_VAL : tiles_time<TO>(a, 256, 2.2);
+  const double best = fmin(fmin(few, t64), fmin(t128, t256));
+  if (best == few)
+    enqueue_rows<2, 4, TO>(a, s);
+  else if (best == t64)
+    enqueue_tiles<64, exact, TO>(a, s);
+  else if (best == t128)
+    enqueue_tiles<128, exact, TO>(a, s);
+  else if constexpr (!exact)
+    enqueue_tiles<256, false, TO>(a, s);
 }
 
 }  // namespace
