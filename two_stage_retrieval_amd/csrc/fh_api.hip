@@ -599,21 +599,19 @@ int dense_impl(const void* E, int64_t v, int32_t d, int32_t dtype, int64_t lde, 
                int32_t B, int32_t mode, float tau, const uint64_t* seeds, int32_t* out_tokens,
                float* out_lse, void* workspace, bool clear_counters, void* stream);
 
-// The workspace of flashhead_verify, laid out from `base` (null: only its
-// size in bytes is wanted).
-size_t verify_layout(VerifyArgs& a, int B, uint8_t* base) {
+// The workspace of flashhead_verify for a's rows, sequences and chunks, laid
+// out from `base` (null: only its size in bytes is wanted).
+size_t verify_layout(VerifyArgs& a, uint8_t* base) {
   size_t at = 0;
   auto take = [&](size_t n) {
     uint8_t* p = base ? base + at : nullptr;
     at += (n + 15) / 16 * 16;
     return p;
   };
-  const size_t parts = (size_t)a.rows * (size_t)a.nchunk, seqs = (size_t)B;
-  a.part_sum = reinterpret_cast<double*>(take(parts * sizeof(double)));
-  a.part_weight = reinterpret_cast<double*>(take(seqs * (size_t)a.nchunk * sizeof(double)));
-  a.state = reinterpret_cast<VerifyState*>(take(seqs * sizeof(VerifyState)));
-  a.part_top = reinterpret_cast<float*>(take(parts * sizeof(float)));
-  a.part_best = reinterpret_cast<int32_t*>(take(parts * sizeof(int32_t)));
+  const size_t rows = (size_t)a.rows, seqs = (size_t)a.B, chunks = (size_t)a.nchunk;
+  a.part = reinterpret_cast<VerifyPart*>(take(rows * chunks * sizeof(VerifyPart)));
+  a.part_weight = reinterpret_cast<double*>(take(seqs * chunks * sizeof(double)));
+  a.arrived = reinterpret_cast<uint32_t*>(take(seqs * sizeof(uint32_t)));
   return at;
 }
 
@@ -945,11 +943,12 @@ int dense_logits_fp8(const uint8_t* h8, int64_t ldh, const float* h_scale, int64
 
 size_t flashhead_verify_workspace_bytes(int32_t B, int64_t rows, int64_t v) {
   if (B < 0 || rows < 0 || v < 1 || v > (int64_t)INT32_MAX) return 0;
+  // the most chunks any call takes: calls of fewer rows take smaller ones
   VerifyArgs a{};
   a.rows = rows;
-  a.v = v;
-  plan_verify(a);
-  return verify_layout(a, B, nullptr);
+  a.B = B;
+  a.nchunk = (int)((v + kVerifyChunk - 1) / kVerifyChunk);
+  return verify_layout(a, nullptr);
 }
 
 int flashhead_verify(const void* logits, int64_t rows, int64_t v, int32_t dtype, int64_t ldl,
@@ -973,17 +972,18 @@ int flashhead_verify(const void* logits, int64_t rows, int64_t v, int32_t dtype,
   a.q = draft_probs;
   a.ldq = ldq;
   a.sample = mode == FH_MODE_SAMPLE;
-  a.inv_tau = a.sample ? 1.0 / (double)tau : 1.0;
+  a.k = 1.4426950408889634074 / (a.sample ? (double)tau : 1.0);
   a.u_accept = u_accept;
   a.u_sample = u_sample;
   a.max_tokens = max_tokens;
   a.out_tokens = out_tokens;
   a.out_accepted = out_accepted;
   a.out_logp = out_logp;
+  a.B = B;
   plan_verify(a);
-  if (verify_layout(a, B, static_cast<uint8_t*>(workspace)) > workspace_bytes)
+  if (verify_layout(a, static_cast<uint8_t*>(workspace)) > workspace_bytes)
     return FH_ERR_INVALID_ARG;
-  FH_TRY(launch_verify(a, dtype, B, static_cast<hipStream_t>(stream)));
+  FH_TRY(launch_verify(a, dtype, static_cast<hipStream_t>(stream)));
   return FH_OK;
 }
 

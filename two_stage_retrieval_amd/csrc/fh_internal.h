@@ -371,14 +371,11 @@ struct Logits8Args {
 hipError_t launch_logits8(const Logits8Args& a, int out_dtype, hipStream_t s);
 
 // Verification of drafted tokens (fh_verify.hip).
-constexpr int kVerifyMaxUnits = 4;  // 8-value units per thread of a chunk
-enum VerifyKind : int { kVerifyDone = 0, kVerifyPlain = 1, kVerifyResidual = 2 };
-struct VerifyState {     // what the draw of a sequence needs
-  int kind;              // VerifyKind: nothing to draw, from p, from max(p - q, 0)
-  int at;                // accepted drafts
-  int64_t row, draft;    // the row that is drawn from, and its draft
-  float top;             // the row's maximum
-  double sum;            // and its sum of exp((z - top) / tau)
+constexpr int kVerifyChunk = 2048;  // smallest chunk of a row
+struct __align__(16) VerifyPart {  // of a (row, chunk)
+  double sum;   // of exp((z - top) / tau)
+  float top;    // largest logit
+  int best;     // its lowest index
 };
 struct VerifyArgs {
   const uint8_t* logits;
@@ -390,7 +387,7 @@ struct VerifyArgs {
   const float* q;            // n_drafts x v probabilities, or null (one-hot)
   int64_t ldq;
   int sample;
-  double inv_tau;            // 1 / tau (1 for greedy decoding)
+  double k;                  // log2(e) / tau (tau 1 for greedy decoding)
   const float* u_accept;
   const float* u_sample;
   int max_tokens;
@@ -400,15 +397,14 @@ struct VerifyArgs {
   // workspace
   int nchunk, units;         // chunks per row, 8-value units per thread of one
   int64_t chunk;             // values per chunk
-  double* part_sum;          // rows x nchunk
+  VerifyPart* part;          // rows x nchunk
   double* part_weight;       // B x nchunk
-  VerifyState* state;        // B
-  float* part_top;           // rows x nchunk
-  int32_t* part_best;        // rows x nchunk
+  uint32_t* arrived;         // B
+  int B;
 };
 // chunk size for these sizes (units, chunk, nchunk of `a`)
 void plan_verify(VerifyArgs& a);
-hipError_t launch_verify(const VerifyArgs& a, int dtype, int B, hipStream_t s);
+hipError_t launch_verify(const VerifyArgs& a, int dtype, hipStream_t s);
 hipError_t launch_cluster_major_copy(const uint8_t* E, int64_t lde_bytes, const int32_t* c2t,
                                      int64_t v, int64_t row_bytes, uint8_t* Ec, hipStream_t s);
 

@@ -14,10 +14,12 @@
 // (errors of 1e-6) would draw another token than the given u says in a few of
 // a hundred calls.
 //
-// Three launches: per (row, chunk) the maximum, its index and the sum of
-// exponentials; per (sequence, chunk) the decisions, folded from the chunks'
-// records by every workgroup for itself, and the sum of the chosen row's
-// weights; per sequence the chunk that holds the draw and the token in it.
+// Two launches.  Per (row, chunk): the maximum, its index and the sum of
+// exponentials.  Per sequence: the decisions, folded from the chunks' records,
+// then the draw, for which the chunks' sums name the chunk and that chunk's
+// running sum the token.  Only max(p - q, 0) has other chunk sums than p: then
+// a workgroup per chunk decides for itself, sums the chunk's weights, and the
+// sequence's last one draws.
 #include "fh_device.h"
 #include "fh_internal.h"
 
@@ -34,9 +36,26 @@ __device__ __forceinline__ double wave_sum_f64(double x) {
   return x;
 }
 
-// exp(x / tau) for x <= 0, k = 1 / tau
+// 2^((x - top) k) for x <= top; 0 for x = -inf, NaN for NaN.  With y = n + f,
+// n the nearest whole number: 2^n 2^f, 2^f by the polynomial that interpolates
+// it at the ten Chebyshev nodes of [-1/2, 1/2] (relative error below 2e-14).
+// It is a third of the library function's instructions, which set the time of
+// the first launch (64 sequences, 288 rows of 128256: 80 us with that one).
 __device__ __forceinline__ double weight(float x, float top, double k) {
-  return exp(((double)x - (double)top) * k);
+  double y = ((double)x - (double)top) * k;
+  y = y < -1100.0 ? -1100.0 : y;  // (2^-1100 is 0; keeps n in range)
+  const double n = __builtin_rint(y), f = y - n;
+  double p = 1.02059054137655955e-07;
+  p = fma(p, f, 1.32596452448871106e-06);
+  p = fma(p, f, 1.52526729248507372e-05);
+  p = fma(p, f, 1.54034337512510097e-04);
+  p = fma(p, f, 1.33335582007945925e-03);
+  p = fma(p, f, 9.61812919393431262e-03);
+  p = fma(p, f, 5.55041086646516704e-02);
+  p = fma(p, f, 2.40226506956403407e-01);
+  p = fma(p, f, 6.93147180559946174e-01);
+  p = fma(p, f, 1.00000000000001354e+00);
+  return __builtin_amdgcn_ldexp(p, (int)n);
 }
 
 // Values [i, i + 8) of a row of n; past its end -inf (logits) or 0
@@ -77,10 +96,10 @@ __device__ __forceinline__ float load1(const uint8_t* row, int64_t i) {
     return reinterpret_cast<const float*>(row)[i];
 }
 
-// Per (row, chunk): top = the maximum, best = its lowest index, sum = the sum
-// of exp((z - top) / tau).  A NaN or +inf logit makes the sum NaN; a chunk of
-// -inf alone has sum 0.
-template <typename T>
+// The record of a (row, chunk): top = the maximum, best = its lowest index,
+// sum = the sum of exp((z - top) / tau).  A NaN or +inf logit makes the sum
+// NaN; a chunk of -inf alone has sum 0.
+template <typename T, int U>
 __global__ __launch_bounds__(kVThreads) void verify_rows_kernel(const VerifyArgs a) {
   __shared__ float s_top[kVWaves];
   __shared__ double s_sum[kVWaves];
@@ -88,45 +107,50 @@ __global__ __launch_bounds__(kVThreads) void verify_rows_kernel(const VerifyArgs
   const int tid = threadIdx.x, w = tid / kWave;
   const int64_t r = blockIdx.x / (unsigned)a.nchunk;
   const int chunk = blockIdx.x % (unsigned)a.nchunk;
+  // the next launch counts the workgroups of a sequence from zero
+  for (int64_t s = (int64_t)blockIdx.x * kVThreads + tid; s < a.B;
+       s += (int64_t)gridDim.x * kVThreads)
+    a.arrived[s] = 0u;
   const uint8_t* row = a.logits + r * a.l_bytes;
   const int64_t c0 = (int64_t)chunk * a.chunk;
   const int64_t end = c0 + a.chunk < a.v ? c0 + a.chunk : a.v;
-  float x[kVerifyMaxUnits][8];
+  float x[U][8];
   float top = -INFINITY;
+  bool nan = false;
 #pragma unroll
-  for (int i = 0; i < kVerifyMaxUnits; ++i) {
-    load8<T>(row, c0 + (i * kVThreads + tid) * 8, i < a.units ? end : 0, -INFINITY, x[i]);
+  for (int i = 0; i < U; ++i)
+    load8<T>(row, c0 + (i * kVThreads + tid) * 8, end, -INFINITY, x[i]);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) top = fmaxf(top, x[i][j]);
-  }
-  top = wave_max(top);
+  for (int i = 0; i < U; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      top = fmaxf(top, x[i][j]);
+      nan |= x[i][j] != x[i][j];
+    }
+  top = wave_max(nan ? INFINITY : top);  // (a NaN ends as +inf does)
   if ((tid & 63) == 0) s_top[w] = top;
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < kVWaves; ++i) top = fmaxf(top, s_top[i]);
   double sum = 0.0;
   int best = INT32_MAX;
-  if (top == -INFINITY) {  // all masked, or NaN: exp would make NaN of both
+  if (top == INFINITY) {
+    sum = NAN;
+  } else if (top > -INFINITY) {
 #pragma unroll
-    for (int i = 0; i < kVerifyMaxUnits; ++i)
+    for (int i = 0; i < U; ++i) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (x[i][j] != x[i][j]) sum = NAN;
-  } else {
-#pragma unroll
-    for (int i = 0; i < kVerifyMaxUnits; ++i) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        sum += weight(x[i][j], top, a.inv_tau);
-        if (x[i][j] == top) {
-          const int t = (int)(c0 + (i * kVThreads + tid) * 8 + j);
-          best = t < best ? t : best;
-        }
-      }
+      for (int j = 0; j < 8; ++j) sum += weight(x[i][j], top, a.k);
     }
+#pragma unroll
+    for (int i = U - 1; i >= 0; --i) {
+#pragma unroll
+      for (int j = 7; j >= 0; --j)
+        if (x[i][j] == top) best = (int)(c0 + (i * kVThreads + tid) * 8 + j);
+    }
+    sum = wave_sum_f64(sum);
+    best = (int)~wave_max_u32(~(uint32_t)best);
   }
-  sum = wave_sum_f64(sum);
-  best = (int)~wave_max_u32(~(uint32_t)best);
   if ((tid & 63) == 0) {
     s_sum[w] = sum;
     s_best[w] = best;
@@ -137,10 +161,7 @@ __global__ __launch_bounds__(kVThreads) void verify_rows_kernel(const VerifyArgs
       sum += s_sum[i];
       best = s_best[i] < best ? s_best[i] : best;
     }
-    const int64_t o = r * a.nchunk + chunk;
-    a.part_top[o] = top;
-    a.part_sum[o] = sum;
-    a.part_best[o] = best;
+    a.part[r * a.nchunk + chunk] = VerifyPart{sum, top, best};
   }
 }
 
@@ -150,17 +171,28 @@ struct RowFold {
   int best;
   double sum;
 };
+// a chunk's sum, relative to the row's maximum (a chunk without a value has
+// sum 0, or NaN)
+__device__ __forceinline__ double chunk_sum(const VerifyPart& p, float top, double k) {
+  return p.top == -INFINITY ? p.sum : p.sum * weight(p.top, top, k);
+}
 __device__ __forceinline__ RowFold fold_row(const VerifyArgs& a, int64_t r, int lane) {
-  const int64_t o = r * a.nchunk;
+  const VerifyPart* part = a.part + r * a.nchunk;
   RowFold f{-INFINITY, INT32_MAX, 0.0};
-  for (int c = lane; c < a.nchunk; c += kWave) f.top = fmaxf(f.top, a.part_top[o + c]);
-  f.top = wave_max(f.top);
-  for (int c = lane; c < a.nchunk; c += kWave) {
-    const float t = a.part_top[o + c];
-    const double s = a.part_sum[o + c];
-    // a chunk without a value (sum 0) adds nothing; its NaN stays
-    f.sum += t == -INFINITY ? s : s * weight(t, f.top, a.inv_tau);
-    if (t == f.top && a.part_best[o + c] < f.best) f.best = a.part_best[o + c];
+  if (a.nchunk <= kWave) {
+    const VerifyPart p =
+        lane < a.nchunk ? part[lane] : VerifyPart{0.0, -INFINITY, INT32_MAX};
+    f.top = wave_max(p.top);
+    f.sum = chunk_sum(p, f.top, a.k);
+    f.best = p.top == f.top ? p.best : INT32_MAX;
+  } else {
+    for (int c = lane; c < a.nchunk; c += kWave) f.top = fmaxf(f.top, part[c].top);
+    f.top = wave_max(f.top);
+    for (int c = lane; c < a.nchunk; c += kWave) {
+      const VerifyPart p = part[c];
+      f.sum += chunk_sum(p, f.top, a.k);
+      if (p.top == f.top && p.best < f.best) f.best = p.best;
+    }
   }
   f.sum = wave_sum_f64(f.sum);
   f.best = (int)~wave_max_u32(~(uint32_t)f.best);
@@ -168,28 +200,68 @@ __device__ __forceinline__ RowFold fold_row(const VerifyArgs& a, int64_t r, int 
 }
 
 __device__ __forceinline__ float log_prob(float x, const RowFold& f, double k) {
-  return (float)(((double)x - (double)f.top) * k - log(f.sum));
+  return (float)(((double)x - (double)f.top) * (k * 0.693147180559945309) - log(f.sum));
 }
 
-// Per (sequence, chunk): the decisions and, for a sample, the sum of the
-// chosen row's weights over the chunk.
+// The weights of 8 values: p, or what q leaves of it, or p without a token.
+template <typename T>
+struct Weights {
+  const uint8_t* row;
+  const uint8_t* q;   // null: none
+  int64_t skip;       // -1: none
+  int64_t end;
+  float top;
+  double k, scale;    // scale 1 / sum where q is subtracted, else 1
+  __device__ __forceinline__ double at(int64_t t, double* w) const {
+    float x[8], y[8];
+    load8<T>(row, t, end, -INFINITY, x);
+    if (q) load8<float>(q, t, end, 0.0f, y);
+    double sum = 0.0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      double p = weight(x[j], top, k) * scale;
+      if (q)
+        p = fmax(p - (double)y[j], 0.0);
+      else if (t + j == skip)
+        p = 0.0;
+      w[j] = p;
+      sum += p;
+    }
+    return sum;
+  }
+};
+
+// sum over the workgroup (all threads get it)
+__device__ __forceinline__ double group_sum_f64(double x, double* s, int tid) {
+  x = wave_sum_f64(x);
+  if ((tid & 63) == 0) s[tid / kWave] = x;
+  __syncthreads();
+  x = 0.0;
+  for (int i = 0; i < kVWaves; ++i) x += s[i];
+  __syncthreads();
+  return x;
+}
+
+// Per sequence (and chunk, where draft probabilities are given).
 template <typename T>
 __global__ __launch_bounds__(kVThreads) void verify_decide_kernel(const VerifyArgs a) {
-  __shared__ int s_state[kVWaves];   // 0 accepted, 1 the sequence's last token is drawn here
+  __shared__ int s_last[kVWaves];   // 0: the wave's draft was accepted
   __shared__ RowFold s_fold[kVWaves];
   __shared__ int s_token[kVWaves];
   __shared__ float s_logp[kVWaves];
   __shared__ double s_sum[kVWaves];
-  __shared__ int s_bad;
+  __shared__ int s_bad, s_go, s_hit, s_end;
+  __shared__ double s_need;
   const int tid = threadIdx.x, lane = tid & 63, w = tid / kWave;
-  const int per = a.sample ? a.nchunk : 1;  // workgroups a sequence
+  const int per = a.q ? a.nchunk : 1;  // workgroups a sequence
   const int s = blockIdx.x / (unsigned)per, chunk = blockIdx.x % (unsigned)per;
+  const bool writer = chunk == 0;
   const int64_t r0 = a.row_start[s], r1 = a.row_start[s + 1];
   const int64_t d0 = r0 - s;         // the sequence's first draft
   const int64_t n = r1 - r0 - 1;     // its drafts
   bool bad = r0 < 0 || n < 0 || r1 > a.rows || n >= a.max_tokens || d0 < 0 ||
              d0 + n > a.n_drafts;
-  if (!bad) {
+  if (!bad && n > 0) {
     if (tid == 0) s_bad = 0;
     __syncthreads();
     for (int64_t i = tid; i < n; i += kVThreads) {
@@ -199,57 +271,44 @@ __global__ __launch_bounds__(kVThreads) void verify_decide_kernel(const VerifyAr
     __syncthreads();
     bad = s_bad != 0;
   }
-  const bool writer = chunk == 0;
   int32_t* out = a.out_tokens + (int64_t)s * a.max_tokens;
   float* logp = a.out_logp ? a.out_logp + (int64_t)s * a.max_tokens : nullptr;
-  VerifyState* st = a.state + s;
   if (bad) {
     if (writer) {
       for (int i = tid; i < a.max_tokens; i += kVThreads) {
         out[i] = -1;
         if (logp) logp[i] = 0.0f;
       }
-      if (tid == 0) {
-        a.out_accepted[s] = -1;
-        st->kind = kVerifyDone;
-      }
+      if (tid == 0) a.out_accepted[s] = -1;
     }
     return;
   }
+  // the rows in order, four at a time, up to the first whose draft is not taken
   int64_t at = 0;
   RowFold f;
   for (int64_t base = 0;; base += kVWaves) {
     const int64_t i = base + w;
     if (i <= n) {
+      // (requested together with the records)
+      const int x = i < n ? a.draft_tokens[d0 + i] : 0;
+      const float z = load1<T>(a.logits + (r0 + i) * a.l_bytes, x);
+      const float q = a.q && i < n ? a.q[(d0 + i) * a.ldq + x] : 1.0f;
+      const float u = a.sample && i < n ? a.u_accept[d0 + i] : 0.0f;
       const RowFold g = fold_row(a, r0 + i, lane);
       if (lane == 0) {
-        int last = 1;
-        if (i < n) {
-          const int x = a.draft_tokens[d0 + i];
-          const float z = load1<T>(a.logits + (r0 + i) * a.l_bytes, x);
-          bool take = false;
-          if (g.sum > 0.0 && g.sum < INFINITY) {
-            if (a.sample) {
-              const double q = a.q ? (double)a.q[(d0 + i) * a.ldq + x] : 1.0;
-              take = (double)a.u_accept[d0 + i] * q < weight(z, g.top, a.inv_tau) / g.sum;
-            } else {
-              take = x == g.best;
-            }
-          }
-          if (take) {
-            last = 0;
-            s_token[w] = x;
-            if (logp) s_logp[w] = log_prob(z, g, a.inv_tau);
-          }
-        }
-        s_state[w] = last;
+        bool take = i < n && g.sum > 0.0 && g.sum < INFINITY;
+        if (take)
+          take = a.sample ? (double)u * (double)q < weight(z, g.top, a.k) / g.sum : x == g.best;
+        s_last[w] = !take;
         s_fold[w] = g;
+        s_token[w] = x;
+        if (logp && take) s_logp[w] = log_prob(z, g, a.k);
       }
     }
     __syncthreads();
     int hit = -1;
     for (int k = 0; k < kVWaves && base + k <= n; ++k)
-      if (hit < 0 && s_state[k]) hit = k;
+      if (hit < 0 && s_last[k]) hit = k;
     if (writer && tid < (hit >= 0 ? hit : kVWaves)) {
       out[base + tid] = s_token[tid];
       if (logp) logp[base + tid] = s_logp[tid];
@@ -261,121 +320,128 @@ __global__ __launch_bounds__(kVThreads) void verify_decide_kernel(const VerifyAr
     }
     __syncthreads();
   }
-  const bool valid = f.sum > 0.0 && f.sum < INFINITY;
+  const bool draws = a.sample && f.sum > 0.0 && f.sum < INFINITY;
   const bool rejected = at < n;
   if (writer) {
-    // a sample's token is the next launch's
-    const int final_token = valid && !a.sample ? f.best : -1;
-    for (int64_t i = at + tid; i < a.max_tokens; i += kVThreads) {
-      out[i] = i == at ? final_token : -1;
-      if (logp) logp[i] = i == at && final_token >= 0 ? log_prob(f.top, f, a.inv_tau) : 0.0f;
+    for (int64_t i = at + 1 + tid; i < a.max_tokens; i += kVThreads) {
+      out[i] = -1;
+      if (logp) logp[i] = 0.0f;
     }
     if (tid == 0) {
       a.out_accepted[s] = (int)at;
-      st->kind = valid && a.sample ? (rejected ? kVerifyResidual : kVerifyPlain) : kVerifyDone;
-      st->at = (int)at;
-      st->row = r0 + at;
-      st->draft = d0 + at;
-      st->top = f.top;
-      st->sum = f.sum;
+      if (!draws) {
+        const bool some = f.sum > 0.0 && f.sum < INFINITY;
+        out[at] = some ? f.best : -1;
+        if (logp) logp[at] = some ? log_prob(f.top, f, a.k) : 0.0f;
+      }
     }
   }
-  if (!a.sample || !valid || !rejected) return;
-  // the chunk's part of the residual weights
-  const uint8_t* row = a.logits + (r0 + at) * a.l_bytes;
-  const uint8_t* q = a.q ? reinterpret_cast<const uint8_t*>(a.q + (d0 + at) * a.ldq) : nullptr;
-  const int64_t skip = a.q ? -1 : a.draft_tokens[d0 + at];
-  const int64_t c0 = (int64_t)chunk * a.chunk;
-  const int64_t end = c0 + a.chunk < a.v ? c0 + a.chunk : a.v;
-  double sum = 0.0;
-  for (int i = 0; i < a.units; ++i) {
-    const int64_t t = c0 + (i * kVThreads + tid) * 8;
-    float x[8], y[8];
-    load8<T>(row, t, end, -INFINITY, x);
-    if (q) load8<float>(q, t, end, 0.0f, y);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const double p = weight(x[j], f.top, a.inv_tau) / f.sum;
-      sum += q ? fmax(p - (double)y[j], 0.0) : (t + j == skip ? 0.0 : p);
-    }
-  }
-  sum = wave_sum_f64(sum);
-  if (lane == 0) s_sum[w] = sum;
-  __syncthreads();
-  if (tid == 0) {
-    for (int i = 1; i < kVWaves; ++i) sum += s_sum[i];
-    a.part_weight[(int64_t)s * a.nchunk + chunk] = sum;
-  }
-}
+  if (!draws) return;
 
-// Per sequence that draws: the chunk and the token.
-template <typename T>
-__global__ __launch_bounds__(kVThreads) void verify_draw_kernel(const VerifyArgs a) {
-  __shared__ double s_sum[kVWaves];
-  __shared__ double s_before;
-  __shared__ int s_chunk, s_plain, s_token, s_last;
-  const int tid = threadIdx.x, lane = tid & 63, w = tid / kWave;
-  const int s = blockIdx.x;
-  const VerifyState st = a.state[s];
-  if (st.kind == kVerifyDone) return;
-  const double* pw = a.part_weight + (int64_t)s * a.nchunk;
-  const int64_t o = st.row * a.nchunk;
-  // a chunk's share under p
-  auto share = [&](int c) {
-    const float t = a.part_top[o + c];
-    return t == -INFINITY ? 0.0 : a.part_sum[o + c] * weight(t, st.top, a.inv_tau) / st.sum;
+  Weights<T> wt;
+  wt.row = a.logits + (r0 + at) * a.l_bytes;
+  wt.q = rejected && a.q ? reinterpret_cast<const uint8_t*>(a.q + (d0 + at) * a.ldq) : nullptr;
+  wt.skip = rejected && !a.q ? a.draft_tokens[d0 + at] : -1;
+  wt.top = f.top;
+  wt.k = a.k;
+  wt.scale = wt.q ? 1.0 / f.sum : 1.0;
+  double* pw = a.part_weight + (int64_t)s * a.nchunk;
+  auto chunk_weight = [&](int c) {
+    const int64_t c0 = (int64_t)c * a.chunk;
+    wt.end = c0 + a.chunk < a.v ? c0 + a.chunk : a.v;
+    double y[8], sum = 0.0;
+    for (int i = 0; i < a.units; ++i) sum += wt.at(c0 + (i * kVThreads + tid) * 8, y);
+    return group_sum_f64(sum, s_sum, tid);
   };
-  if (tid == 0) {
-    bool plain = st.kind == kVerifyPlain;
-    double total = 0.0;
-    if (!plain) {
-      for (int c = 0; c < a.nchunk; ++c) total += pw[c];
-      plain = !(total > 0.0);  // q covers p everywhere: draw from p
+  if (wt.q) {
+    const double sum = chunk_weight(chunk);
+    if (tid == 0) {
+      // Seen by the whole device before the count goes up; whoever counts the
+      // last one finds all of them.
+      __hip_atomic_store(reinterpret_cast<uint64_t*>(pw + chunk),
+                         (uint64_t)__double_as_longlong(sum), __ATOMIC_RELAXED,
+                         __HIP_MEMORY_SCOPE_AGENT);
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      const uint32_t before = __hip_atomic_fetch_add(a.arrived + s, 1u, __ATOMIC_RELAXED,
+                                                     __HIP_MEMORY_SCOPE_AGENT);
+      s_go = before + 1 == (uint32_t)per;
     }
-    if (plain) {
+    __syncthreads();
+    if (!s_go) return;
+  } else if (!writer) {
+    return;
+  }
+  // a token that p loses: its chunk's sum without it
+  const int skip_chunk = wt.skip >= 0 ? (int)(wt.skip / a.chunk) : -1;
+  double skip_sum = 0.0;
+  if (skip_chunk >= 0) skip_sum = chunk_weight(skip_chunk);
+
+  // the chunk: the first whose running sum passes u times the total (wave 0)
+  if (w == 0) {
+    const VerifyPart* part = a.part + (r0 + at) * a.nchunk;
+    auto get = [&](int c, bool plain) {
+      if (c >= a.nchunk) return 0.0;
+      if (!plain && wt.q)
+        return __longlong_as_double((long long)__hip_atomic_load(
+            reinterpret_cast<uint64_t*>(pw + c), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+      if (!plain && c == skip_chunk) return skip_sum;
+      return chunk_sum(part[c], f.top, a.k);
+    };
+    bool plain = !rejected;
+    double total = 0.0;
+    for (int pass = 0; pass < 2; ++pass) {
       total = 0.0;
-      for (int c = 0; c < a.nchunk; ++c) total += share(c);
+      for (int c = lane; c < a.nchunk; c += kWave) total += get(c, plain);
+      total = wave_sum_f64(total);
+      if (plain || total > 0.0) break;
+      plain = true;  // nothing is left of p: the draw is from p itself
     }
     const double target = fmax((double)a.u_sample[s], 0.0) * total;
-    double before = 0.0;
-    int hit = -1, last = 0;
-    double last_before = 0.0;
-    for (int c = 0; c < a.nchunk && hit < 0; ++c) {
-      const double x = plain ? share(c) : pw[c];
-      if (before + x > target) hit = c;
-      if (x > 0.0) { last = c; last_before = before; }
-      if (hit < 0) before += x;
+    double before = 0.0, need = 0.0;
+    int hit = -1, end = 0;   // end: the last chunk with a weight
+    for (int c0 = 0; c0 < a.nchunk && hit < 0; c0 += kWave) {
+      const double x = get(c0 + lane, plain);
+      double scan = x;
+#pragma unroll
+      for (int d = 1; d < kWave; d <<= 1) {
+        const double up = __shfl_up(scan, d, kWave);
+        if (lane >= d) scan += up;
+      }
+      scan += before;
+      const uint64_t over = __ballot(x > 0.0 && scan > target), some = __ballot(x > 0.0);
+      // (rounding can leave no chunk over the target: then the last one, with
+      // a need that its running sum may not pass either)
+      const int l = over ? (int)__builtin_ctzll(over) : some ? 63 - __builtin_clzll(some) : -1;
+      if (l >= 0) {
+        end = c0 + l;
+        need = target - __shfl(scan - x, l, kWave);
+        if (over) hit = end;
+      }
+      before = __shfl(scan, 63, kWave);
     }
-    if (hit < 0) { hit = last; before = last_before; }
-    s_chunk = hit;
-    s_plain = plain;
-    s_before = target - before;  // what the chunk's running sum has to pass
-    s_token = INT32_MAX;
-    s_last = -1;
+    if (lane == 0) {
+      s_hit = INT32_MAX;
+      s_end = -1;
+      s_token[0] = end;
+      s_token[1] = plain;
+      s_need = need;
+    }
   }
   __syncthreads();
-  const bool plain = s_plain;
-  const double need = s_before;
-  const uint8_t* row = a.logits + st.row * a.l_bytes;
-  const uint8_t* q =
-      a.q && !plain ? reinterpret_cast<const uint8_t*>(a.q + st.draft * a.ldq) : nullptr;
-  const int64_t skip = a.q || plain ? -1 : a.draft_tokens[st.draft];
-  const int64_t c0 = (int64_t)s_chunk * a.chunk;
-  const int64_t end = c0 + a.chunk < a.v ? c0 + a.chunk : a.v;
+  const int64_t c0 = (int64_t)s_token[0] * a.chunk;
+  const double need = s_need;
+  if (s_token[1]) {
+    wt.q = nullptr;
+    wt.skip = -1;
+    wt.scale = 1.0;
+  }
+  wt.end = c0 + a.chunk < a.v ? c0 + a.chunk : a.v;
+  // the token: the first whose running sum passes what is left of the target
   double before = 0.0;
   for (int i = 0; i < a.units; ++i) {
     const int64_t t = c0 + (i * kVThreads + tid) * 8;
-    float x[8], y[8];
-    double wt[8], sum = 0.0;
-    load8<T>(row, t, end, -INFINITY, x);
-    if (q) load8<float>(q, t, end, 0.0f, y);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const double p = weight(x[j], st.top, a.inv_tau) / st.sum;
-      wt[j] = q ? fmax(p - (double)y[j], 0.0) : (t + j == skip ? 0.0 : p);
-      sum += wt[j];
-    }
-    // running sum before this thread's values
+    double y[8];
+    const double sum = wt.at(t, y);
     double scan = sum;
 #pragma unroll
     for (int d = 1; d < kWave; d <<= 1) {
@@ -390,52 +456,51 @@ __global__ __launch_bounds__(kVThreads) void verify_draw_kernel(const VerifyArgs
     int hit = INT32_MAX, last = -1;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      c += wt[j];
-      if (wt[j] > 0.0) {
+      c += y[j];
+      if (y[j] > 0.0) {
         last = (int)(t + j);
         if (c > need && hit == INT32_MAX) hit = (int)(t + j);
       }
     }
-    if (hit != INT32_MAX) atomicMin(&s_token, hit);
-    if (last >= 0) atomicMax(&s_last, last);
+    if (hit != INT32_MAX) atomicMin(&s_hit, hit);
+    if (last >= 0) atomicMax(&s_end, last);
     __syncthreads();
-    if (s_token != INT32_MAX) break;
+    if (s_hit != INT32_MAX) break;
   }
   if (tid == 0) {
-    const int t = s_token != INT32_MAX ? s_token : s_last;
-    const int64_t i = (int64_t)s * a.max_tokens + st.at;
-    a.out_tokens[i] = t;
-    if (a.out_logp && t >= 0) {
-      const RowFold f{st.top, 0, st.sum};
-      a.out_logp[i] = log_prob(load1<T>(row, t), f, a.inv_tau);
-    }
+    const int t = s_hit != INT32_MAX ? s_hit : s_end;
+    out[at] = t;
+    if (logp) logp[at] = t >= 0 ? log_prob(load1<T>(wt.row, t), f, a.k) : 0.0f;
   }
 }
 
 template <typename T>
-void enqueue(const VerifyArgs& a, int B, hipStream_t s) {
+void enqueue(const VerifyArgs& a, hipStream_t s) {
   const dim3 block(kVThreads);
   const unsigned n = (unsigned)a.nchunk;
-  if (a.rows)
-    hipLaunchKernelGGL(verify_rows_kernel<T>, dim3((unsigned)a.rows * n), block, 0, s, a);
-  hipLaunchKernelGGL(verify_decide_kernel<T>, dim3((unsigned)B * (a.sample ? n : 1u)), block, 0, s,
+  if (a.rows && a.units == 1)
+    hipLaunchKernelGGL((verify_rows_kernel<T, 1>), dim3((unsigned)a.rows * n), block, 0, s, a);
+  else if (a.rows)
+    hipLaunchKernelGGL((verify_rows_kernel<T, 2>), dim3((unsigned)a.rows * n), block, 0, s, a);
+  hipLaunchKernelGGL(verify_decide_kernel<T>, dim3((unsigned)a.B * (a.q ? n : 1u)), block, 0, s,
                      a);
-  if (a.sample) hipLaunchKernelGGL(verify_draw_kernel<T>, dim3((unsigned)B), block, 0, s, a);
 }
 
 }  // namespace
 
+// Chunks of 4096 values where they make at least 512 workgroups (two a compute
+// unit), else of 2048, so that short batches still reach most compute units.
 void plan_verify(VerifyArgs& a) {
-  a.units = 2;
+  a.units = a.rows * ((a.v + 4095) / 4096) >= 512 ? 2 : 1;
   a.chunk = (int64_t)a.units * kVThreads * 8;
   a.nchunk = (int)((a.v + a.chunk - 1) / a.chunk);
 }
 
-hipError_t launch_verify(const VerifyArgs& a, int dtype, int B, hipStream_t s) {
+hipError_t launch_verify(const VerifyArgs& a, int dtype, hipStream_t s) {
   if (dtype == FH_DTYPE_BF16)
-    enqueue<uint16_t>(a, B, s);
+    enqueue<uint16_t>(a, s);
   else
-    enqueue<float>(a, B, s);
+    enqueue<float>(a, s);
   return hipGetLastError();
 }
 
