@@ -398,8 +398,9 @@ int dense_logits_fp8(const uint8_t* h8, int64_t ldh, const float* h_scale, int64
  *            with w_0 + .. + w_t > u_sample[s] * (w_0 + .. + w_{v-1}).
  *   greedy   x_j is accepted while it is the lowest argmax of its row, which
  *            is also the next token.
- * The comparisons and sums are in fp64, so the result is the one the given
- * numbers determine, on every call.  With n = 0 the call is a plain draw.
+ * The comparisons and sums are in fp64 (a probability below 2^-1020 of the
+ * row's largest counts as 0), so the result is the one the given numbers
+ * determine, on every call.  With n = 0 the call is a plain draw.
  *   logits        device, rows x v, FH_DTYPE_*, rows at multiples of 16 bytes
  *                 (v itself may be any size).  -inf marks a token that
  *                 cannot occur.  A row of -inf alone, or with a NaN or +inf,

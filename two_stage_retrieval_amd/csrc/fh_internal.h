@@ -377,6 +377,13 @@ struct __align__(16) VerifyPart {  // of a (row, chunk)
   float top;    // largest logit
   int best;     // its lowest index
 };
+struct VerifyState {     // of a sequence that draws from max(p - q, 0)
+  int64_t row, draft;    // p's row, and q's
+  double sum;            // p's sum of exp((z - top) / tau)
+  float top;             // p's largest logit
+  int at;                // accepted drafts
+  int draws;             // 0: nothing is left to do
+};
 struct VerifyArgs {
   const uint8_t* logits;
   int64_t l_bytes;
@@ -400,6 +407,7 @@ struct VerifyArgs {
   VerifyPart* part;          // rows x nchunk
   double* part_weight;       // B x nchunk
   uint32_t* arrived;         // B
+  VerifyState* state;        // B
   int B;
 };
 // chunk size for these sizes (units, chunk, nchunk of `a`)

@@ -14,12 +14,15 @@
 // (errors of 1e-6) would draw another token than the given u says in a few of
 // a hundred calls.
 //
-// Two launches.  Per (row, chunk): the maximum, its index and the sum of
-// exponentials.  Per sequence: the decisions, folded from the chunks' records,
-// then the draw, for which the chunks' sums name the chunk and that chunk's
-// running sum the token.  Only max(p - q, 0) has other chunk sums than p: then
-// a workgroup per chunk decides for itself, sums the chunk's weights, and the
-// sequence's last one draws.
+// First launch, per (row, chunk): the maximum, its index and the sum of
+// exponentials.  Second, per sequence: the decisions, folded from the chunks'
+// records, then the draw, for which the chunks' sums name the chunk and that
+// chunk's running sum the token.  Only max(p - q, 0) has other chunk sums than
+// p: then a workgroup per chunk sums the chunk's weights, and the sequence's
+// last one draws.  Those decide for themselves in the second launch where
+// they all fit the device at once (one sequence of four drafts, 128256: 19 us
+// in two launches); where they do not (64 sequences: 41 us, mostly the same
+// decisions made 32 times over), a third launch takes over the second's state.
 #include "fh_device.h"
 #include "fh_internal.h"
 
@@ -27,8 +30,10 @@ namespace fh {
 
 namespace {
 
-constexpr int kVThreads = 256;
+constexpr int kVThreads = 256;  // of the first launch
 constexpr int kVWaves = kVThreads / kWave;
+constexpr int kDThreads = 512;  // of the others: a chunk is 8 values a thread
+constexpr int kDWaves = kDThreads / kWave;
 
 __device__ __forceinline__ double wave_sum_f64(double x) {
 #pragma unroll
@@ -36,15 +41,18 @@ __device__ __forceinline__ double wave_sum_f64(double x) {
   return x;
 }
 
-// 2^((x - top) k) for x <= top; 0 for x = -inf, NaN for NaN.  With y = n + f,
-// n the nearest whole number: 2^n 2^f, 2^f by the polynomial that interpolates
-// it at the ten Chebyshev nodes of [-1/2, 1/2] (relative error below 2e-14).
-// It is a third of the library function's instructions, which set the time of
-// the first launch (64 sequences, 288 rows of 128256: 80 us with that one).
+// 2^((x - top) k) for x <= top, not NaN; kZero: 0 from 2^-1020 on, else at
+// least about that (enough for a sum that holds a 1).  With y = n + f, n the
+// nearest whole number, it is 2^f with n added to the exponent; n is the low
+// word of y + 1.5 * 2^52, and 2^f the polynomial that interpolates it at the
+// ten Chebyshev nodes of [-1/2, 1/2] (relative error below 2e-14).  These
+// instructions set the time of the first launch: 288 rows of 128256 took 80 us
+// with the library's exp and 42 with the conversions to and from n.
+template <bool kZero = true>
 __device__ __forceinline__ double weight(float x, float top, double k) {
   double y = ((double)x - (double)top) * k;
-  y = y < -1100.0 ? -1100.0 : y;  // (2^-1100 is 0; keeps n in range)
-  const double n = __builtin_rint(y), f = y - n;
+  if constexpr (!kZero) y = fmax(y, -1020.0);
+  const double n = y + 6755399441055744.0, f = y - (n - 6755399441055744.0);
   double p = 1.02059054137655955e-07;
   p = fma(p, f, 1.32596452448871106e-06);
   p = fma(p, f, 1.52526729248507372e-05);
@@ -55,7 +63,9 @@ __device__ __forceinline__ double weight(float x, float top, double k) {
   p = fma(p, f, 2.40226506956403407e-01);
   p = fma(p, f, 6.93147180559946174e-01);
   p = fma(p, f, 1.00000000000001354e+00);
-  return __builtin_amdgcn_ldexp(p, (int)n);
+  p = __hiloint2double(__double2hiint(p) + (__double2loint(n) << 20), __double2loint(p));
+  if constexpr (kZero) p = y < -1020.0 ? 0.0 : p;
+  return p;
 }
 
 // Values [i, i + 8) of a row of n; past its end -inf (logits) or 0
@@ -140,7 +150,7 @@ __global__ __launch_bounds__(kVThreads) void verify_rows_kernel(const VerifyArgs
 #pragma unroll
     for (int i = 0; i < U; ++i) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sum += weight(x[i][j], top, a.k);
+      for (int j = 0; j < 8; ++j) sum += weight<false>(x[i][j], top, a.k);
     }
 #pragma unroll
     for (int i = U - 1; i >= 0; --i) {
@@ -172,9 +182,9 @@ struct RowFold {
   double sum;
 };
 // a chunk's sum, relative to the row's maximum (a chunk without a value has
-// sum 0, or NaN)
+// sum 0)
 __device__ __forceinline__ double chunk_sum(const VerifyPart& p, float top, double k) {
-  return p.top == -INFINITY ? p.sum : p.sum * weight(p.top, top, k);
+  return p.top == -INFINITY ? 0.0 : p.sum * weight(p.top, top, k);
 }
 __device__ __forceinline__ RowFold fold_row(const VerifyArgs& a, int64_t r, int lane) {
   const VerifyPart* part = a.part + r * a.nchunk;
@@ -203,17 +213,17 @@ __device__ __forceinline__ float log_prob(float x, const RowFold& f, double k) {
   return (float)(((double)x - (double)f.top) * (k * 0.693147180559945309) - log(f.sum));
 }
 
-// The weights of 8 values: p, or what q leaves of it, or p without a token.
+// The weights of 8 values (p, or what q leaves of it, or p without a token)
+// and their sum; x: the logits.
 template <typename T>
 struct Weights {
   const uint8_t* row;
   const uint8_t* q;   // null: none
   int64_t skip;       // -1: none
-  int64_t end;
   float top;
   double k, scale;    // scale 1 / sum where q is subtracted, else 1
-  __device__ __forceinline__ double at(int64_t t, double* w) const {
-    float x[8], y[8];
+  __device__ __forceinline__ double at(int64_t t, int64_t end, float* x, double* w) const {
+    float y[8];
     load8<T>(row, t, end, -INFINITY, x);
     if (q) load8<float>(q, t, end, 0.0f, y);
     double sum = 0.0;
@@ -231,127 +241,151 @@ struct Weights {
   }
 };
 
-// sum over the workgroup (all threads get it)
-__device__ __forceinline__ double group_sum_f64(double x, double* s, int tid) {
-  x = wave_sum_f64(x);
-  if ((tid & 63) == 0) s[tid / kWave] = x;
-  __syncthreads();
-  x = 0.0;
-  for (int i = 0; i < kVWaves; ++i) x += s[i];
-  __syncthreads();
-  return x;
-}
+enum VerifyMode { kAll, kDecide, kDraw };
 
-// Per sequence (and chunk, where draft probabilities are given).
-template <typename T>
-__global__ __launch_bounds__(kVThreads) void verify_decide_kernel(const VerifyArgs a) {
-  __shared__ int s_last[kVWaves];   // 0: the wave's draft was accepted
-  __shared__ RowFold s_fold[kVWaves];
-  __shared__ int s_token[kVWaves];
-  __shared__ float s_logp[kVWaves];
-  __shared__ double s_sum[kVWaves];
-  __shared__ int s_bad, s_go, s_hit, s_end;
+// kAll: a workgroup per (sequence, chunk); kDecide: one per sequence, which
+// also draws unless q is to be subtracted; kDraw: per (sequence, chunk), the
+// draws that kDecide left.
+template <typename T, VerifyMode kMode>
+__global__ __launch_bounds__(kDThreads) void verify_decide_kernel(const VerifyArgs a) {
+  __shared__ int s_last[kDWaves];   // 0: the wave's draft was accepted
+  __shared__ RowFold s_fold[kDWaves];
+  __shared__ int s_token[kDWaves];
+  __shared__ float s_logp[kDWaves];
+  __shared__ double s_sum[kDWaves];
+  __shared__ int s_go, s_hit, s_end, s_chunk, s_plain;
   __shared__ double s_need;
   const int tid = threadIdx.x, lane = tid & 63, w = tid / kWave;
-  const int per = a.q ? a.nchunk : 1;  // workgroups a sequence
+  const int per = kMode == kDecide ? 1 : a.nchunk;  // workgroups a sequence
   const int s = blockIdx.x / (unsigned)per, chunk = blockIdx.x % (unsigned)per;
-  const bool writer = chunk == 0;
-  const int64_t r0 = a.row_start[s], r1 = a.row_start[s + 1];
-  const int64_t d0 = r0 - s;         // the sequence's first draft
-  const int64_t n = r1 - r0 - 1;     // its drafts
-  bool bad = r0 < 0 || n < 0 || r1 > a.rows || n >= a.max_tokens || d0 < 0 ||
-             d0 + n > a.n_drafts;
-  if (!bad && n > 0) {
-    if (tid == 0) s_bad = 0;
-    __syncthreads();
-    for (int64_t i = tid; i < n; i += kVThreads) {
-      const int x = a.draft_tokens[d0 + i];
-      if (x < 0 || (int64_t)x >= a.v) s_bad = 1;
-    }
-    __syncthreads();
-    bad = s_bad != 0;
-  }
   int32_t* out = a.out_tokens + (int64_t)s * a.max_tokens;
   float* logp = a.out_logp ? a.out_logp + (int64_t)s * a.max_tokens : nullptr;
-  if (bad) {
+  int64_t row, draft;   // what is drawn from
+  int at;               // accepted drafts
+  bool rejected;
+  RowFold f;
+  if constexpr (kMode == kDraw) {
+    const VerifyState st = a.state[s];
+    if (!st.draws) return;
+    row = st.row;
+    draft = st.draft;
+    at = st.at;
+    rejected = true;
+    f = RowFold{st.top, 0, st.sum};
+  } else {
+    const bool writer = chunk == 0;
+    const int64_t r0 = a.row_start[s], r1 = a.row_start[s + 1];
+    const int64_t d0 = r0 - s;         // the sequence's first draft
+    const int64_t n = r1 - r0 - 1;     // its drafts
+    bool bad = r0 < 0 || n < 0 || r1 > a.rows || n >= a.max_tokens || d0 < 0 ||
+               d0 + n > a.n_drafts;
+    int64_t base = 0;
+    if (!bad) {
+      bool far = false;
+      for (int64_t i = tid; i < n; i += kDThreads) {
+        const int x = a.draft_tokens[d0 + i];
+        far |= x < 0 || (int64_t)x >= a.v;
+      }
+      // the rows in order, eight at a time, up to the first whose draft is not
+      // taken
+      for (;; base += kDWaves) {
+        const int64_t i = base + w;
+        if (i <= n) {
+          // (requested together with the records; a draft outside the
+          // vocabulary is seen to below)
+          const int x = i < n ? a.draft_tokens[d0 + i] : 0;
+          const int64_t xi = x < 0 ? 0 : (int64_t)x < a.v ? x : a.v - 1;
+          const float z = load1<T>(a.logits + (r0 + i) * a.l_bytes, xi);
+          const float q = a.q && i < n ? a.q[(d0 + i) * a.ldq + xi] : 1.0f;
+          const float u = a.sample && i < n ? a.u_accept[d0 + i] : 0.0f;
+          const RowFold g = fold_row(a, r0 + i, lane);
+          if (lane == 0) {
+            bool take = i < n && g.sum > 0.0 && g.sum < INFINITY;
+            if (take)
+              take = a.sample ? (double)u * (double)q < weight(z, g.top, a.k) / g.sum
+                              : x == g.best;
+            s_last[w] = !take;
+            s_fold[w] = g;
+            s_token[w] = x;
+            if (logp && take) s_logp[w] = log_prob(z, g, a.k);
+          }
+        }
+        if (base == 0)
+          bad = __syncthreads_or(far);
+        else
+          __syncthreads();
+        if (bad) break;
+        int hit = -1;
+        for (int k = 0; k < kDWaves && base + k <= n; ++k)
+          if (hit < 0 && s_last[k]) hit = k;
+        if (writer && tid < (hit >= 0 ? hit : kDWaves)) {
+          out[base + tid] = s_token[tid];
+          if (logp) logp[base + tid] = s_logp[tid];
+        }
+        if (hit >= 0) {
+          at = (int)base + hit;
+          f = s_fold[hit];
+          break;
+        }
+        __syncthreads();
+      }
+    }
+    if (bad) {
+      if (writer) {
+        for (int i = tid; i < a.max_tokens; i += kDThreads) {
+          out[i] = -1;
+          if (logp) logp[i] = 0.0f;
+        }
+        if (tid == 0) {
+          a.out_accepted[s] = -1;
+          if (kMode == kDecide && a.q) a.state[s].draws = 0;
+        }
+      }
+      return;
+    }
+    const bool some = f.sum > 0.0 && f.sum < INFINITY;  // the row has a distribution
+    rejected = at < n;
+    row = r0 + at;
+    draft = d0 + at;
     if (writer) {
-      for (int i = tid; i < a.max_tokens; i += kVThreads) {
+      for (int64_t i = at + 1 + tid; i < a.max_tokens; i += kDThreads) {
         out[i] = -1;
         if (logp) logp[i] = 0.0f;
       }
-      if (tid == 0) a.out_accepted[s] = -1;
-    }
-    return;
-  }
-  // the rows in order, four at a time, up to the first whose draft is not taken
-  int64_t at = 0;
-  RowFold f;
-  for (int64_t base = 0;; base += kVWaves) {
-    const int64_t i = base + w;
-    if (i <= n) {
-      // (requested together with the records)
-      const int x = i < n ? a.draft_tokens[d0 + i] : 0;
-      const float z = load1<T>(a.logits + (r0 + i) * a.l_bytes, x);
-      const float q = a.q && i < n ? a.q[(d0 + i) * a.ldq + x] : 1.0f;
-      const float u = a.sample && i < n ? a.u_accept[d0 + i] : 0.0f;
-      const RowFold g = fold_row(a, r0 + i, lane);
-      if (lane == 0) {
-        bool take = i < n && g.sum > 0.0 && g.sum < INFINITY;
-        if (take)
-          take = a.sample ? (double)u * (double)q < weight(z, g.top, a.k) / g.sum : x == g.best;
-        s_last[w] = !take;
-        s_fold[w] = g;
-        s_token[w] = x;
-        if (logp && take) s_logp[w] = log_prob(z, g, a.k);
+      if (tid == 0) {
+        a.out_accepted[s] = at;
+        if (!some || !a.sample) {
+          out[at] = some ? f.best : -1;
+          if (logp) logp[at] = some ? log_prob(f.top, f, a.k) : 0.0f;
+        }
+        if (kMode == kDecide && a.q)
+          a.state[s] = VerifyState{row, draft, f.sum, f.top, at, some && rejected};
       }
     }
-    __syncthreads();
-    int hit = -1;
-    for (int k = 0; k < kVWaves && base + k <= n; ++k)
-      if (hit < 0 && s_last[k]) hit = k;
-    if (writer && tid < (hit >= 0 ? hit : kVWaves)) {
-      out[base + tid] = s_token[tid];
-      if (logp) logp[base + tid] = s_logp[tid];
-    }
-    if (hit >= 0) {
-      at = base + hit;
-      f = s_fold[hit];
-      break;
-    }
-    __syncthreads();
+    if (!some || !a.sample) return;
+    if (rejected && a.q ? kMode == kDecide : !writer) return;
   }
-  const bool draws = a.sample && f.sum > 0.0 && f.sum < INFINITY;
-  const bool rejected = at < n;
-  if (writer) {
-    for (int64_t i = at + 1 + tid; i < a.max_tokens; i += kVThreads) {
-      out[i] = -1;
-      if (logp) logp[i] = 0.0f;
-    }
-    if (tid == 0) {
-      a.out_accepted[s] = (int)at;
-      if (!draws) {
-        const bool some = f.sum > 0.0 && f.sum < INFINITY;
-        out[at] = some ? f.best : -1;
-        if (logp) logp[at] = some ? log_prob(f.top, f, a.k) : 0.0f;
-      }
-    }
-  }
-  if (!draws) return;
 
   Weights<T> wt;
-  wt.row = a.logits + (r0 + at) * a.l_bytes;
-  wt.q = rejected && a.q ? reinterpret_cast<const uint8_t*>(a.q + (d0 + at) * a.ldq) : nullptr;
-  wt.skip = rejected && !a.q ? a.draft_tokens[d0 + at] : -1;
+  wt.row = a.logits + row * a.l_bytes;
+  wt.q = rejected && a.q ? reinterpret_cast<const uint8_t*>(a.q + draft * a.ldq) : nullptr;
+  wt.skip = rejected && !a.q ? a.draft_tokens[draft] : -1;
   wt.top = f.top;
   wt.k = a.k;
   wt.scale = wt.q ? 1.0 / f.sum : 1.0;
   double* pw = a.part_weight + (int64_t)s * a.nchunk;
+  float x[8];
+  double y[8];
+  // a chunk's weights, this thread's 8 of them in y; the sum is thread 0's
   auto chunk_weight = [&](int c) {
     const int64_t c0 = (int64_t)c * a.chunk;
-    wt.end = c0 + a.chunk < a.v ? c0 + a.chunk : a.v;
-    double y[8], sum = 0.0;
-    for (int i = 0; i < a.units; ++i) sum += wt.at(c0 + (i * kVThreads + tid) * 8, y);
-    return group_sum_f64(sum, s_sum, tid);
+    const int64_t end = c0 + a.chunk < a.v ? c0 + a.chunk : a.v;
+    double sum = wave_sum_f64(wt.at(c0 + tid * 8, end, x, y));
+    if (lane == 0) s_sum[w] = sum;
+    __syncthreads();
+    if (tid == 0)
+      for (int i = 1; i < kDWaves; ++i) sum += s_sum[i];
+    return sum;
   };
   if (wt.q) {
     const double sum = chunk_weight(chunk);
@@ -368,17 +402,16 @@ __global__ __launch_bounds__(kVThreads) void verify_decide_kernel(const VerifyAr
     }
     __syncthreads();
     if (!s_go) return;
-  } else if (!writer) {
-    return;
   }
   // a token that p loses: its chunk's sum without it
   const int skip_chunk = wt.skip >= 0 ? (int)(wt.skip / a.chunk) : -1;
   double skip_sum = 0.0;
   if (skip_chunk >= 0) skip_sum = chunk_weight(skip_chunk);
 
-  // the chunk: the first whose running sum passes u times the total (wave 0)
+  // the chunk: the first whose running sum passes u times the total
   if (w == 0) {
-    const VerifyPart* part = a.part + (r0 + at) * a.nchunk;
+    skip_sum = __shfl(skip_sum, 0, kWave);
+    const VerifyPart* part = a.part + row * a.nchunk;
     auto get = [&](int c, bool plain) {
       if (c >= a.nchunk) return 0.0;
       if (!plain && wt.q)
@@ -387,103 +420,108 @@ __global__ __launch_bounds__(kVThreads) void verify_decide_kernel(const VerifyAr
       if (!plain && c == skip_chunk) return skip_sum;
       return chunk_sum(part[c], f.top, a.k);
     };
+    const float u = a.u_sample[s];
     bool plain = !rejected;
     double total = 0.0;
-    for (int pass = 0; pass < 2; ++pass) {
+    for (;;) {
       total = 0.0;
       for (int c = lane; c < a.nchunk; c += kWave) total += get(c, plain);
       total = wave_sum_f64(total);
       if (plain || total > 0.0) break;
       plain = true;  // nothing is left of p: the draw is from p itself
     }
-    const double target = fmax((double)a.u_sample[s], 0.0) * total;
+    const double target = fmax((double)u, 0.0) * total;
     double before = 0.0, need = 0.0;
-    int hit = -1, end = 0;   // end: the last chunk with a weight
-    for (int c0 = 0; c0 < a.nchunk && hit < 0; c0 += kWave) {
-      const double x = get(c0 + lane, plain);
-      double scan = x;
+    int end = 0;   // the chunk, or the last one with a weight
+    bool hit = false;
+    for (int c0 = 0; c0 < a.nchunk && !hit; c0 += kWave) {
+      const double p = get(c0 + lane, plain);
+      double scan = p;
 #pragma unroll
       for (int d = 1; d < kWave; d <<= 1) {
         const double up = __shfl_up(scan, d, kWave);
         if (lane >= d) scan += up;
       }
       scan += before;
-      const uint64_t over = __ballot(x > 0.0 && scan > target), some = __ballot(x > 0.0);
+      const uint64_t over = __ballot(p > 0.0 && scan > target), some = __ballot(p > 0.0);
       // (rounding can leave no chunk over the target: then the last one, with
       // a need that its running sum may not pass either)
       const int l = over ? (int)__builtin_ctzll(over) : some ? 63 - __builtin_clzll(some) : -1;
       if (l >= 0) {
         end = c0 + l;
-        need = target - __shfl(scan - x, l, kWave);
-        if (over) hit = end;
+        need = target - __shfl(scan - p, l, kWave);
+        hit = over != 0;
       }
       before = __shfl(scan, 63, kWave);
     }
     if (lane == 0) {
       s_hit = INT32_MAX;
       s_end = -1;
-      s_token[0] = end;
-      s_token[1] = plain;
+      s_chunk = end;
+      s_plain = plain;
       s_need = need;
     }
   }
   __syncthreads();
-  const int64_t c0 = (int64_t)s_token[0] * a.chunk;
-  const double need = s_need;
-  if (s_token[1]) {
+  if (s_plain) {
     wt.q = nullptr;
     wt.skip = -1;
     wt.scale = 1.0;
   }
-  wt.end = c0 + a.chunk < a.v ? c0 + a.chunk : a.v;
   // the token: the first whose running sum passes what is left of the target
-  double before = 0.0;
-  for (int i = 0; i < a.units; ++i) {
-    const int64_t t = c0 + (i * kVThreads + tid) * 8;
-    double y[8];
-    const double sum = wt.at(t, y);
-    double scan = sum;
+  const double need = s_need;
+  const int64_t c0 = (int64_t)s_chunk * a.chunk, t = c0 + tid * 8;
+  const double sum = wt.at(t, c0 + a.chunk < a.v ? c0 + a.chunk : a.v, x, y);
+  double scan = sum;
 #pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) {
-      const double up = __shfl_up(scan, d, kWave);
-      if (lane >= d) scan += up;
-    }
-    if (lane == 63) s_sum[w] = scan;
-    __syncthreads();
-    double c = before + (scan - sum);
-    for (int k = 0; k < w; ++k) c += s_sum[k];
-    for (int k = 0; k < kVWaves; ++k) before += s_sum[k];
-    int hit = INT32_MAX, last = -1;
+  for (int d = 1; d < kWave; d <<= 1) {
+    const double up = __shfl_up(scan, d, kWave);
+    if (lane >= d) scan += up;
+  }
+  if (lane == 63) s_sum[w] = scan;
+  __syncthreads();
+  double c = scan - sum;
+  for (int k = 0; k < w; ++k) c += s_sum[k];
+  int hit = INT32_MAX, last = -1;
+  float hit_x = 0.0f, last_x = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      c += y[j];
-      if (y[j] > 0.0) {
-        last = (int)(t + j);
-        if (c > need && hit == INT32_MAX) hit = (int)(t + j);
+  for (int j = 0; j < 8; ++j) {
+    c += y[j];
+    if (y[j] > 0.0) {
+      last = (int)(t + j);
+      last_x = x[j];
+      if (c > need && hit == INT32_MAX) {
+        hit = last;
+        hit_x = x[j];
       }
     }
-    if (hit != INT32_MAX) atomicMin(&s_hit, hit);
-    if (last >= 0) atomicMax(&s_end, last);
-    __syncthreads();
-    if (s_hit != INT32_MAX) break;
   }
-  if (tid == 0) {
-    const int t = s_hit != INT32_MAX ? s_hit : s_end;
-    out[at] = t;
-    if (logp) logp[at] = t >= 0 ? log_prob(load1<T>(wt.row, t), f, a.k) : 0.0f;
+  if (hit != INT32_MAX) atomicMin(&s_hit, hit);
+  if (last >= 0) atomicMax(&s_end, last);
+  __syncthreads();
+  const int token = s_hit != INT32_MAX ? s_hit : s_end;
+  if (token == hit || (s_hit == INT32_MAX && token == last)) {  // the thread that has it
+    out[at] = token;
+    if (logp) logp[at] = log_prob(token == hit ? hit_x : last_x, f, a.k);
   }
 }
 
 template <typename T>
 void enqueue(const VerifyArgs& a, hipStream_t s) {
-  const dim3 block(kVThreads);
-  const unsigned n = (unsigned)a.nchunk;
+  const unsigned n = (unsigned)a.nchunk, B = (unsigned)a.B;
   if (a.rows && a.units == 1)
-    hipLaunchKernelGGL((verify_rows_kernel<T, 1>), dim3((unsigned)a.rows * n), block, 0, s, a);
+    hipLaunchKernelGGL((verify_rows_kernel<T, 1>), dim3((unsigned)a.rows * n), dim3(kVThreads), 0,
+                       s, a);
   else if (a.rows)
-    hipLaunchKernelGGL((verify_rows_kernel<T, 2>), dim3((unsigned)a.rows * n), block, 0, s, a);
-  hipLaunchKernelGGL(verify_decide_kernel<T>, dim3((unsigned)a.B * (a.q ? n : 1u)), block, 0, s,
-                     a);
+    hipLaunchKernelGGL((verify_rows_kernel<T, 2>), dim3((unsigned)a.rows * n), dim3(kVThreads), 0,
+                       s, a);
+  if (a.q && (int64_t)B * n <= 512) {
+    hipLaunchKernelGGL((verify_decide_kernel<T, kAll>), dim3(B * n), dim3(kDThreads), 0, s, a);
+    return;
+  }
+  hipLaunchKernelGGL((verify_decide_kernel<T, kDecide>), dim3(B), dim3(kDThreads), 0, s, a);
+  if (a.q)
+    hipLaunchKernelGGL((verify_decide_kernel<T, kDraw>), dim3(B * n), dim3(kDThreads), 0, s, a);
 }
 
 }  // namespace
