@@ -35,11 +35,27 @@ constexpr int kVWaves = kVThreads / kWave;
 constexpr int kDThreads = 512;  // of the others: a chunk is 8 values a thread
 constexpr int kDWaves = kDThreads / kWave;
 
-__device__ __forceinline__ double wave_sum_f64(double x) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) x += __shfl_xor(x, o, kWave);
+// Running sum over the wave, in lane order, on DPP (both words of a value move
+// by the same control; lanes without a source add 0).  Every lane is active.
+__device__ __forceinline__ double wave_scan_f64(double x) {
+#define FH_DPP_ADD(ctrl, rmask)                                                                 \
+  x += __hiloint2double(                                                                        \
+      __builtin_amdgcn_update_dpp(0, __double2hiint(x), ctrl, rmask, 0xf, false),               \
+      __builtin_amdgcn_update_dpp(0, __double2loint(x), ctrl, rmask, 0xf, false));
+  FH_DPP_ADD(0x111, 0xf)  // row_shr:1
+  FH_DPP_ADD(0x112, 0xf)  // row_shr:2
+  FH_DPP_ADD(0x114, 0xf)  // row_shr:4
+  FH_DPP_ADD(0x118, 0xf)  // row_shr:8
+  FH_DPP_ADD(0x142, 0xa)  // row_bcast:15 into rows 1 and 3
+  FH_DPP_ADD(0x143, 0xc)  // row_bcast:31 into rows 2 and 3
+#undef FH_DPP_ADD
   return x;
 }
+__device__ __forceinline__ double lane_f64(double x, int lane) {
+  return __hiloint2double(__builtin_amdgcn_readlane(__double2hiint(x), lane),
+                          __builtin_amdgcn_readlane(__double2loint(x), lane));
+}
+__device__ __forceinline__ double wave_sum_f64(double x) { return lane_f64(wave_scan_f64(x), 63); }
 
 // 2^((x - top) k) for x <= top, not NaN; kZero: 0 from 2^-1020 on, else at
 // least about that (enough for a sum that holds a 1).  With y = n + f, n the
@@ -253,7 +269,8 @@ __global__ __launch_bounds__(kDThreads) void verify_decide_kernel(const VerifyAr
   __shared__ int s_token[kDWaves];
   __shared__ float s_logp[kDWaves];
   __shared__ double s_sum[kDWaves];
-  __shared__ int s_go, s_hit, s_end, s_chunk, s_plain;
+  __shared__ int s_pass[kDWaves];
+  __shared__ int s_go, s_chunk, s_plain;
   __shared__ double s_need;
   const int tid = threadIdx.x, lane = tid & 63, w = tid / kWave;
   const int per = kMode == kDecide ? 1 : a.nchunk;  // workgroups a sequence
@@ -302,12 +319,12 @@ __global__ __launch_bounds__(kDThreads) void verify_decide_kernel(const VerifyAr
           if (lane == 0) {
             bool take = i < n && g.sum > 0.0 && g.sum < INFINITY;
             if (take)
-              take = a.sample ? (double)u * (double)q < weight(z, g.top, a.k) / g.sum
+              take = a.sample ? (double)u * (double)q * g.sum < weight(z, g.top, a.k)
                               : x == g.best;
             s_last[w] = !take;
             s_fold[w] = g;
             s_token[w] = x;
-            if (logp && take) s_logp[w] = log_prob(z, g, a.k);
+            if (logp && take && writer) s_logp[w] = log_prob(z, g, a.k);
           }
         }
         if (base == 0)
@@ -410,7 +427,7 @@ __global__ __launch_bounds__(kDThreads) void verify_decide_kernel(const VerifyAr
 
   // the chunk: the first whose running sum passes u times the total
   if (w == 0) {
-    skip_sum = __shfl(skip_sum, 0, kWave);
+    skip_sum = lane_f64(skip_sum, 0);
     const VerifyPart* part = a.part + row * a.nchunk;
     auto get = [&](int c, bool plain) {
       if (c >= a.nchunk) return 0.0;
@@ -436,27 +453,19 @@ __global__ __launch_bounds__(kDThreads) void verify_decide_kernel(const VerifyAr
     bool hit = false;
     for (int c0 = 0; c0 < a.nchunk && !hit; c0 += kWave) {
       const double p = get(c0 + lane, plain);
-      double scan = p;
-#pragma unroll
-      for (int d = 1; d < kWave; d <<= 1) {
-        const double up = __shfl_up(scan, d, kWave);
-        if (lane >= d) scan += up;
-      }
-      scan += before;
+      const double scan = before + wave_scan_f64(p);
       const uint64_t over = __ballot(p > 0.0 && scan > target), some = __ballot(p > 0.0);
       // (rounding can leave no chunk over the target: then the last one, with
       // a need that its running sum may not pass either)
       const int l = over ? (int)__builtin_ctzll(over) : some ? 63 - __builtin_clzll(some) : -1;
       if (l >= 0) {
         end = c0 + l;
-        need = target - __shfl(scan - p, l, kWave);
+        need = target - lane_f64(scan - p, l);
         hit = over != 0;
       }
-      before = __shfl(scan, 63, kWave);
+      before = lane_f64(scan, 63);
     }
     if (lane == 0) {
-      s_hit = INT32_MAX;
-      s_end = -1;
       s_chunk = end;
       s_plain = plain;
       s_need = need;
@@ -472,17 +481,12 @@ __global__ __launch_bounds__(kDThreads) void verify_decide_kernel(const VerifyAr
   const double need = s_need;
   const int64_t c0 = (int64_t)s_chunk * a.chunk, t = c0 + tid * 8;
   const double sum = wt.at(t, c0 + a.chunk < a.v ? c0 + a.chunk : a.v, x, y);
-  double scan = sum;
-#pragma unroll
-  for (int d = 1; d < kWave; d <<= 1) {
-    const double up = __shfl_up(scan, d, kWave);
-    if (lane >= d) scan += up;
-  }
+  const double scan = wave_scan_f64(sum);
   if (lane == 63) s_sum[w] = scan;
   __syncthreads();
   double c = scan - sum;
   for (int k = 0; k < w; ++k) c += s_sum[k];
-  int hit = INT32_MAX, last = -1;
+  int hit = -1, last = -1;
   float hit_x = 0.0f, last_x = 0.0f;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
@@ -490,19 +494,27 @@ __global__ __launch_bounds__(kDThreads) void verify_decide_kernel(const VerifyAr
     if (y[j] > 0.0) {
       last = (int)(t + j);
       last_x = x[j];
-      if (c > need && hit == INT32_MAX) {
+      if (c > need && hit < 0) {
         hit = last;
         hit_x = x[j];
       }
     }
   }
-  if (hit != INT32_MAX) atomicMin(&s_hit, hit);
-  if (last >= 0) atomicMax(&s_end, last);
+  // tokens rise with the lane and the wave: the first wave's first lane that
+  // passed, or (where rounding left none) the last one's last with a weight
+  const uint64_t hits = __ballot(hit >= 0), lasts = __ballot(last >= 0);
+  if (lane == 0) s_pass[w] = (hits ? 1 : 0) | (lasts ? 2 : 0);
   __syncthreads();
-  const int token = s_hit != INT32_MAX ? s_hit : s_end;
-  if (token == hit || (s_hit == INT32_MAX && token == last)) {  // the thread that has it
-    out[at] = token;
-    if (logp) logp[at] = log_prob(token == hit ? hit_x : last_x, f, a.k);
+  int first = -1, end = -1;
+  for (int k = kDWaves - 1; k >= 0; --k) {
+    if (s_pass[k] & 1) first = k;
+    if ((s_pass[k] & 2) && end < 0) end = k;
+  }
+  const bool mine = first >= 0 ? w == first && lane == (int)__builtin_ctzll(hits | 1ull << 63)
+                               : w == end && lane == 63 - (int)__builtin_clzll(lasts | 1ull);
+  if (mine) {
+    out[at] = first >= 0 ? hit : last;
+    if (logp) logp[at] = log_prob(first >= 0 ? hit_x : last_x, f, a.k);
   }
 }
 
