@@ -149,14 +149,17 @@ class FakeDevice:
     """Stands for a tensor on a second device (none is needed to refuse it)."""
 
     def __init__(self, t, index):
-        self._t, self.is_cuda, self.device = t, True, torch.device("cuda", index)
+        self._t, self.device = t, torch.device("cuda", index)
+
+    def get_device(self):
+        return self.device.index
 
     def __getattr__(self, name):
         return getattr(self._t, name)
 
 
 def test_binding_refuses_other_devices(fh, monkeypatch):
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(fh, "_current_device", lambda: 0)
     x = torch.zeros(4, 256)
     with pytest.raises(ValueError, match="current device"):
         fh.flashhead_rmsnorm(FakeDevice(x, 1), y=FakeDevice(x, 1))

@@ -206,43 +206,74 @@ def dtype_code(t) -> int:
     raise TypeError(f"unsupported dtype {t.dtype}")
 
 
-def _matrix(t, what: str, rows=None, cols=None, dtypes=None, like=None):
-    """Checks a device matrix (unit stride along a row) and returns its
-    address and row stride in elements; (None, 0) for None.  `like`: a tensor
-    of the same call whose device it must share."""
+# The calls around the head check every tensor they pass on.  Those that fit
+# are told in one comparison each (about 0.5 us a tensor; the GPU's part of a
+# small call is 3 us), and _refuse says what was wrong with one that does not.
+
+class _Kinds:
+    """torch's types in tuples, and its stream and device lookups, once."""
+
+    def __init__(self):
+        torch = _torch()
+        self.f32, self.i32, self.u8 = (torch.float32,), (torch.int32,), (torch.uint8,)
+        self.f8 = (torch.float8_e4m3fn,)
+        self.value = (torch.float32, torch.bfloat16)
+        self.code = {torch.float32: FH_DTYPE_F32, torch.bfloat16: FH_DTYPE_BF16}
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        self.stream = raw or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+_kinds_once = None
+
+
+def _kinds() -> _Kinds:
+    global _kinds_once
+    if _kinds_once is None:
+        _kinds_once = _Kinds()
+    return _kinds_once
+
+
+def _current_device() -> int:
+    return _torch().cuda.current_device()
+
+
+def _check_current(dev: int, what: str) -> None:
+    if dev < 0:
+        raise ValueError(f"{what}: a device tensor is expected")
+    if dev != _current_device():
+        raise ValueError(f"{what}: on device {dev}, which is not the current device")
+
+
+def _refuse(t, what: str, dev: int, kinds, shape) -> None:
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype not in kinds:
+        raise TypeError(f"{what}: unsupported dtype {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{what}: on {t.device}, other arguments on device {dev}")
+    raise ValueError(f"{what}: strides {t.stride()}, rows must be contiguous and not overlap")
+
+
+def _matrix(t, what: str, dev: int, kinds, rows: int, cols: int):
+    """(address, row stride in elements) of a rows x cols matrix on device
+    dev whose rows are contiguous; (None, 0) for None."""
     if t is None:
         return None, 0
-    if t.dim() != 2 or (rows is not None and t.shape[0] != rows) or \
-            (cols is not None and t.shape[1] != cols):
-        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected "
-                         f"({'rows' if rows is None else rows}, {'columns' if cols is None else cols})")
-    ld = t.stride(0)
-    if t.shape[1] > 1 and t.stride(1) != 1 or t.shape[0] > 1 and ld < t.shape[1]:
-        raise ValueError(f"{what}: strides {t.stride()}, rows must be contiguous and not overlap")
-    _on_device(t, what, dtypes, like)
+    if t.shape != (rows, cols) or t.dtype not in kinds or t.get_device() != dev:
+        _refuse(t, what, dev, kinds, (rows, cols))
+    ld, one = t.stride()
+    if one != 1 and cols > 1 or ld < cols and rows > 1:
+        _refuse(t, what, dev, kinds, (rows, cols))
     return t.data_ptr(), ld
 
 
-def _vector(t, what: str, n: int, dtypes, like=None):
-    """Checks a contiguous device vector and returns its address; None for None."""
+def _vector(t, what: str, dev: int, kinds, n: int):
+    """Address of n contiguous values on device dev; None for None."""
     if t is None:
         return None
-    if t.numel() != n or not t.is_contiguous():
-        raise ValueError(f"{what}: {n} contiguous values expected, got shape {tuple(t.shape)}")
-    _on_device(t, what, dtypes, like)
+    if t.numel() != n or t.dtype not in kinds or t.get_device() != dev or not t.is_contiguous():
+        _refuse(t, what, dev, kinds, (n,))
     return t.data_ptr()
-
-
-def _on_device(t, what: str, dtypes, like) -> None:
-    if dtypes is not None and t.dtype not in dtypes:
-        raise TypeError(f"{what}: unsupported dtype {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{what}: a device tensor is expected, got one on {t.device}")
-    if like is not None:
-        if t.device != like.device:
-            raise ValueError(f"{what}: on {t.device}, other arguments on {like.device}")
-    elif t.device.index != _torch().cuda.current_device():
-        raise ValueError(f"{what}: on {t.device}, which is not the current device")
 
 
 def _debug(dbg: Optional[dict]):
@@ -388,48 +419,56 @@ def flashhead_rmsnorm(x, weight=None, *, residual=None, residual_out=None, y=Non
     """RMS norm of the rows of x (+ residual) into the given outputs: t = x +
     residual, y in x's dtype, y8 (torch.float8_e4m3fn) with y_scale per 128
     columns."""
-    torch = _torch()
-    kinds = (torch.float32, torch.bfloat16)
-    xp, ldx = _matrix(x, "x", dtypes=kinds)
+    k = _kinds()
     rows, d = x.shape
-    same = (x.dtype,)
-    rp, ldr = _matrix(residual, "residual", rows, d, same, x)
-    wp = _vector(weight, "weight", d, same, x)
-    op, ldro = _matrix(residual_out, "residual_out", rows, d, same, x)
-    yp, ldy = _matrix(y, "y", rows, d, same, x)
-    qp, ldq = _matrix(y8, "y8", rows, d, (torch.float8_e4m3fn,), x)
-    sp, lds = _matrix(y_scale, "y_scale", rows, -(-d // FH_FP8_BLOCK), (torch.float32,), x)
-    _check(lib.flashhead_rmsnorm(xp, ldx, rp, ldr, wp, rows, d, dtype_code(x), eps,
-                                 weight_offset, op, ldro, yp, ldy, qp, ldq, sp, lds,
-                                 _stream(stream)), "flashhead_rmsnorm")
+    dev, kind = x.get_device(), (x.dtype,)
+    xp, ldx = _matrix(x, "x", dev, k.value, rows, d)
+    _check_current(dev, "x")
+    rp, ldr = _matrix(residual, "residual", dev, kind, rows, d)
+    wp = _vector(weight, "weight", dev, kind, d)
+    op, ldro = _matrix(residual_out, "residual_out", dev, kind, rows, d)
+    yp, ldy = _matrix(y, "y", dev, kind, rows, d)
+    qp, ldq = _matrix(y8, "y8", dev, k.f8, rows, d)
+    sp, lds = _matrix(y_scale, "y_scale", dev, k.f32, rows, -(-d // FH_FP8_BLOCK))
+    st = lib.flashhead_rmsnorm(xp, ldx, rp, ldr, wp, rows, d, k.code[x.dtype], eps,
+                               weight_offset, op, ldro, yp, ldy, qp, ldq, sp, lds,
+                               k.stream(dev) if stream is None else stream)
+    if st:
+        _check(st, "flashhead_rmsnorm")
 
 
 def flashhead_quantize_fp8(E, E8, E_scale, stream=None) -> None:
     """E in torch.float8_e4m3fn codes E8 with a scale per 128 x 128 block."""
-    torch = _torch()
-    ep, lde = _matrix(E, "E", dtypes=(torch.float32, torch.bfloat16))
+    k = _kinds()
     v, d = E.shape
-    qp, ldq = _matrix(E8, "E8", v, d, (torch.float8_e4m3fn,), E)
-    sp, lds = _matrix(E_scale, "E_scale", -(-v // FH_FP8_BLOCK), -(-d // FH_FP8_BLOCK),
-                      (torch.float32,), E)
-    _check(lib.flashhead_quantize_fp8(ep, v, d, dtype_code(E), lde, qp, ldq, sp, lds,
-                                      _stream(stream)), "flashhead_quantize_fp8")
+    dev = E.get_device()
+    ep, lde = _matrix(E, "E", dev, k.value, v, d)
+    _check_current(dev, "E")
+    qp, ldq = _matrix(E8, "E8", dev, k.f8, v, d)
+    sp, lds = _matrix(E_scale, "E_scale", dev, k.f32, -(-v // FH_FP8_BLOCK),
+                      -(-d // FH_FP8_BLOCK))
+    st = lib.flashhead_quantize_fp8(ep, v, d, k.code[E.dtype], lde, qp, ldq, sp, lds,
+                                    k.stream(dev) if stream is None else stream)
+    if st:
+        _check(st, "flashhead_quantize_fp8")
 
 
 def dense_logits_fp8(h8, h_scale, E8, E_scale, out, stream=None) -> None:
     """out (rows x v, fp32 or bf16) = the logits of 8-bit h and E."""
-    torch = _torch()
-    f8, f32 = (torch.float8_e4m3fn,), (torch.float32,)
-    hp, ldh = _matrix(h8, "h8", dtypes=f8)
+    k = _kinds()
     rows, d = h8.shape
-    g = -(-d // FH_FP8_BLOCK)
-    ep, lde = _matrix(E8, "E8", None, d, f8, h8)
-    v = E8.shape[0]
-    hs, lds = _matrix(h_scale, "h_scale", rows, g, f32, h8)
-    es, ldes = _matrix(E_scale, "E_scale", -(-v // FH_FP8_BLOCK), g, f32, h8)
-    op, ldo = _matrix(out, "out", rows, v, (torch.float32, torch.bfloat16), h8)
-    _check(lib.dense_logits_fp8(hp, ldh, hs, lds, rows, ep, lde, es, ldes, v, d, op,
-                                dtype_code(out), ldo, _stream(stream)), "dense_logits_fp8")
+    v, g, dev = E8.shape[0], -(-d // FH_FP8_BLOCK), h8.get_device()
+    hp, ldh = _matrix(h8, "h8", dev, k.f8, rows, d)
+    _check_current(dev, "h8")
+    hs, lds = _matrix(h_scale, "h_scale", dev, k.f32, rows, g)
+    ep, lde = _matrix(E8, "E8", dev, k.f8, v, d)
+    es, ldes = _matrix(E_scale, "E_scale", dev, k.f32, -(-v // FH_FP8_BLOCK), g)
+    op, ldo = _matrix(out, "out", dev, k.value, rows, v)
+    st = lib.dense_logits_fp8(hp, ldh, hs, lds, rows, ep, lde, es, ldes, v, d, op,
+                              k.code[out.dtype], ldo,
+                              k.stream(dev) if stream is None else stream)
+    if st:
+        _check(st, "dense_logits_fp8")
 
 
 def flashhead_verify_workspace_bytes(B: int, rows: int, v: int) -> int:
@@ -441,28 +480,30 @@ def flashhead_verify(logits, row_start, draft_tokens, out_tokens, out_accepted, 
                      u_accept=None, u_sample=None, out_logp=None, stream=None) -> None:
     """Verification of drafted tokens against the target's logits (rows x v)
     from given uniform numbers; row_start holds B + 1 offsets."""
-    torch = _torch()
-    i32, f32 = (torch.int32,), (torch.float32,)
-    lp, ldl = _matrix(logits, "logits", dtypes=(torch.float32, torch.bfloat16))
+    k = _kinds()
     rows, v = logits.shape
+    dev = logits.get_device()
     B, n = row_start.numel() - 1, draft_tokens.numel()
     if B < 0:
         raise ValueError("row_start: at least one offset is expected")
-    rp = _vector(row_start, "row_start", B + 1, i32, logits)
-    dp = _vector(draft_tokens, "draft_tokens", n, i32, logits)
-    qp, ldq = _matrix(draft_probs, "draft_probs", n, v, f32, logits)
-    ap = _vector(u_accept, "u_accept", n, f32, logits)
-    up = _vector(u_sample, "u_sample", B, f32, logits)
-    tp, ldt = _matrix(out_tokens, "out_tokens", B, None, i32, logits)
-    m = out_tokens.shape[1]
-    op, ldo = _matrix(out_logp, "out_logp", B, m, f32, logits)
-    if B > 1 and (ldt != m or out_logp is not None and ldo != m):
-        raise ValueError("out_tokens and out_logp must be contiguous")
-    cp = _vector(out_accepted, "out_accepted", B, i32, logits)
-    wp = _vector(workspace, "workspace", workspace.numel(), (torch.uint8,), logits)
-    _check(lib.flashhead_verify(lp, rows, v, dtype_code(logits), ldl, rp, B, dp, n, qp, ldq, mode,
-                                tau, ap, up, m, tp, cp, op, wp, workspace.numel(),
-                                _stream(stream)), "flashhead_verify")
+    m = out_tokens.shape[-1]
+    lp, ldl = _matrix(logits, "logits", dev, k.value, rows, v)
+    _check_current(dev, "logits")
+    rp = _vector(row_start, "row_start", dev, k.i32, B + 1)
+    dp = _vector(draft_tokens, "draft_tokens", dev, k.i32, n)
+    qp, ldq = _matrix(draft_probs, "draft_probs", dev, k.f32, n, v)
+    ap = _vector(u_accept, "u_accept", dev, k.f32, n)
+    up = _vector(u_sample, "u_sample", dev, k.f32, B)
+    tp = _vector(out_tokens, "out_tokens", dev, k.i32, B * m)
+    op = _vector(out_logp, "out_logp", dev, k.f32, B * m)
+    cp = _vector(out_accepted, "out_accepted", dev, k.i32, B)
+    bytes_ = workspace.numel()
+    wp = _vector(workspace, "workspace", dev, k.u8, bytes_)
+    st = lib.flashhead_verify(lp, rows, v, k.code[logits.dtype], ldl, rp, B, dp, n, qp, ldq, mode,
+                              tau, ap, up, m, tp, cp, op, wp, bytes_,
+                              k.stream(dev) if stream is None else stream)
+    if st:
+        _check(st, "flashhead_verify")
 
 
 def flashhead_kmeans(E, c: int, init, max_iter: int, out_c2t, out_centroids=None, *,
