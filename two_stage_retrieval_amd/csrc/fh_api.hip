@@ -599,9 +599,10 @@ int dense_impl(const void* E, int64_t v, int32_t d, int32_t dtype, int64_t lde, 
                int32_t B, int32_t mode, float tau, const uint64_t* seeds, int32_t* out_tokens,
                float* out_lse, void* workspace, bool clear_counters, void* stream);
 
-// The workspace of flashhead_verify for a's rows, sequences and chunks, laid
-// out from `base` (null: only its size in bytes is wanted).
+// The chunks of a call of flashhead_verify, and its workspace laid out from
+// `base` (null: only its size in bytes is wanted).
 size_t verify_layout(VerifyArgs& a, uint8_t* base) {
+  a.nchunk = (int)((a.v + kVerifyChunk - 1) / kVerifyChunk);
   size_t at = 0;
   auto take = [&](size_t n) {
     uint8_t* p = base ? base + at : nullptr;
@@ -944,11 +945,10 @@ int dense_logits_fp8(const uint8_t* h8, int64_t ldh, const float* h_scale, int64
 
 size_t flashhead_verify_workspace_bytes(int32_t B, int64_t rows, int64_t v) {
   if (B < 0 || rows < 0 || v < 1 || v > (int64_t)INT32_MAX) return 0;
-  // the most chunks any call takes: calls of fewer rows take smaller ones
   VerifyArgs a{};
   a.rows = rows;
+  a.v = v;
   a.B = B;
-  a.nchunk = (int)((v + kVerifyChunk - 1) / kVerifyChunk);
   return verify_layout(a, nullptr);
 }
 
@@ -981,7 +981,6 @@ int flashhead_verify(const void* logits, int64_t rows, int64_t v, int32_t dtype,
   a.out_accepted = out_accepted;
   a.out_logp = out_logp;
   a.B = B;
-  plan_verify(a);
   if (verify_layout(a, static_cast<uint8_t*>(workspace)) > workspace_bytes)
     return FH_ERR_INVALID_ARG;
   FH_TRY(launch_verify(a, dtype, static_cast<hipStream_t>(stream)));

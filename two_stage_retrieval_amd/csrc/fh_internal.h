@@ -371,7 +371,7 @@ struct Logits8Args {
 hipError_t launch_logits8(const Logits8Args& a, int out_dtype, hipStream_t s);
 
 // Verification of drafted tokens (fh_verify.hip).
-constexpr int kVerifyChunk = 2048;  // smallest chunk of a row
+constexpr int kVerifyChunk = 2048;  // values of a row that are summed together
 struct __align__(16) VerifyPart {  // of a (row, chunk)
   double sum;   // of exp((z - top) / tau)
   float top;    // largest logit
@@ -402,16 +402,13 @@ struct VerifyArgs {
   int32_t* out_accepted;     // B
   float* out_logp;           // B x max_tokens, or null
   // workspace
-  int nchunk, units;         // chunks per row, 8-value units per thread of one
-  int64_t chunk;             // values per chunk
+  int nchunk;                // chunks per row
   VerifyPart* part;          // rows x nchunk
   double* part_weight;       // B x nchunk
   uint32_t* arrived;         // B
   VerifyState* state;        // B
   int B;
 };
-// chunk size for these sizes (units, chunk, nchunk of `a`)
-void plan_verify(VerifyArgs& a);
 hipError_t launch_verify(const VerifyArgs& a, int dtype, hipStream_t s);
 hipError_t launch_cluster_major_copy(const uint8_t* E, int64_t lde_bytes, const int32_t* c2t,
                                      int64_t v, int64_t row_bytes, uint8_t* Ec, hipStream_t s);

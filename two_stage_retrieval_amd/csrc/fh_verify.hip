@@ -32,8 +32,9 @@ namespace {
 
 constexpr int kVThreads = 256;  // of the first launch
 constexpr int kVWaves = kVThreads / kWave;
-constexpr int kDThreads = 512;  // of the others: a chunk is 8 values a thread
-constexpr int kDWaves = kDThreads / kWave;
+// A chunk is 8 values a thread of the draws; the decisions have a wave for each
+// of 8 rows.
+constexpr int kDrawThreads = kVerifyChunk / 8, kDecideThreads = 512;
 
 // Running sum over the wave, in lane order, on DPP (both words of a value move
 // by the same control; lanes without a source add 0).  Every lane is active.
@@ -84,22 +85,26 @@ __device__ __forceinline__ double weight(float x, float top, double k) {
   return p;
 }
 
-// Values [i, i + 8) of a row of n; past its end -inf (logits) or 0
-// (probabilities), without reading there.
+// Values [i, i + 8) of a row.
+template <typename T>
+__device__ __forceinline__ void load_whole8(const uint8_t* row, int64_t i, float* x) {
+  if constexpr (sizeof(T) == 2) {
+    const uint4 w = *reinterpret_cast<const uint4*>(row + i * 2);
+    x[0] = bf16_lo(w.x); x[1] = bf16_hi(w.x); x[2] = bf16_lo(w.y); x[3] = bf16_hi(w.y);
+    x[4] = bf16_lo(w.z); x[5] = bf16_hi(w.z); x[6] = bf16_lo(w.w); x[7] = bf16_hi(w.w);
+  } else {
+    const float4 a = *reinterpret_cast<const float4*>(row + i * 4);
+    const float4 b = *reinterpret_cast<const float4*>(row + i * 4 + 16);
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+  }
+}
+// The same of a row of n: past its end `fill`, without reading there.
 template <typename T>
 __device__ __forceinline__ void load8(const uint8_t* row, int64_t i, int64_t n, float fill,
                                       float* x) {
   if (i + 8 <= n) {
-    if constexpr (sizeof(T) == 2) {
-      const uint4 w = *reinterpret_cast<const uint4*>(row + i * 2);
-      x[0] = bf16_lo(w.x); x[1] = bf16_hi(w.x); x[2] = bf16_lo(w.y); x[3] = bf16_hi(w.y);
-      x[4] = bf16_lo(w.z); x[5] = bf16_hi(w.z); x[6] = bf16_lo(w.w); x[7] = bf16_hi(w.w);
-    } else {
-      const float4 a = *reinterpret_cast<const float4*>(row + i * 4);
-      const float4 b = *reinterpret_cast<const float4*>(row + i * 4 + 16);
-      x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-      x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-    }
+    load_whole8<T>(row, i, x);
     return;
   }
 #pragma unroll
@@ -122,73 +127,65 @@ __device__ __forceinline__ float load1(const uint8_t* row, int64_t i) {
     return reinterpret_cast<const float*>(row)[i];
 }
 
-// The record of a (row, chunk): top = the maximum, best = its lowest index,
-// sum = the sum of exp((z - top) / tau).  A NaN or +inf logit makes the sum
-// NaN; a chunk of -inf alone has sum 0.
-template <typename T, int U>
+// The record of a (row, chunk), one wave each: top = the maximum, best = its
+// lowest index (kBest; greedy decoding), sum = the sum of exp((z - top) / tau).
+// A NaN or +inf logit makes the sum NaN; a chunk of -inf alone has sum 0.
+// A lane holds 32 values, so that the wave's reductions are a tenth of the
+// work, and no wave waits for another.
+template <typename T, bool kBest>
 __global__ __launch_bounds__(kVThreads) void verify_rows_kernel(const VerifyArgs a) {
-  __shared__ float s_top[kVWaves];
-  __shared__ double s_sum[kVWaves];
-  __shared__ int s_best[kVWaves];
-  const int tid = threadIdx.x, w = tid / kWave;
-  const int64_t r = blockIdx.x / (unsigned)a.nchunk;
-  const int chunk = blockIdx.x % (unsigned)a.nchunk;
+  constexpr int U = kVerifyChunk / (kWave * 8);
+  const int tid = threadIdx.x, lane = tid & 63;
   // the next launch counts the workgroups of a sequence from zero
   for (int64_t s = (int64_t)blockIdx.x * kVThreads + tid; s < a.B;
        s += (int64_t)gridDim.x * kVThreads)
     a.arrived[s] = 0u;
+  const int64_t id = (int64_t)blockIdx.x * kVWaves + __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int64_t r = id / a.nchunk;
+  if (r >= a.rows) return;
   const uint8_t* row = a.logits + r * a.l_bytes;
-  const int64_t c0 = (int64_t)chunk * a.chunk;
-  const int64_t end = c0 + a.chunk < a.v ? c0 + a.chunk : a.v;
+  const int64_t c0 = (id - r * a.nchunk) * kVerifyChunk;
+  const int64_t end = c0 + kVerifyChunk < a.v ? c0 + kVerifyChunk : a.v;
   float x[U][8];
   float top = -INFINITY;
   bool nan = false;
+  if (c0 + kVerifyChunk <= a.v) {
+#pragma unroll
+    for (int i = 0; i < U; ++i) load_whole8<T>(row, c0 + (i * kWave + lane) * 8, x[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+      load8<T>(row, c0 + (i * kWave + lane) * 8, end, -INFINITY, x[i]);
+  }
 #pragma unroll
   for (int i = 0; i < U; ++i)
-    load8<T>(row, c0 + (i * kVThreads + tid) * 8, end, -INFINITY, x[i]);
 #pragma unroll
-  for (int i = 0; i < U; ++i)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      top = fmaxf(top, x[i][j]);
-      nan |= x[i][j] != x[i][j];
+    for (int j = 0; j < 8; j += 2) {
+      top = fmaxf(top, fmaxf(x[i][j], x[i][j + 1]));
+      nan |= __builtin_isunordered(x[i][j], x[i][j + 1]);
     }
   top = wave_max(nan ? INFINITY : top);  // (a NaN ends as +inf does)
-  if ((tid & 63) == 0) s_top[w] = top;
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kVWaves; ++i) top = fmaxf(top, s_top[i]);
   double sum = 0.0;
   int best = INT32_MAX;
   if (top == INFINITY) {
     sum = NAN;
   } else if (top > -INFINITY) {
+    double part[2] = {0.0, 0.0};
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
+    for (int i = 0; i < U; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sum += weight<false>(x[i][j], top, a.k);
+      for (int j = 0; j < 8; ++j) part[j & 1] += weight<false>(x[i][j], top, a.k);
+    sum = wave_sum_f64(part[0] + part[1]);
+    if constexpr (kBest) {
+#pragma unroll
+      for (int i = U - 1; i >= 0; --i)
+#pragma unroll
+        for (int j = 7; j >= 0; --j)
+          if (x[i][j] == top) best = (int)(c0 + (i * kWave + lane) * 8 + j);
+      best = (int)~wave_max_u32(~(uint32_t)best);
     }
-#pragma unroll
-    for (int i = U - 1; i >= 0; --i) {
-#pragma unroll
-      for (int j = 7; j >= 0; --j)
-        if (x[i][j] == top) best = (int)(c0 + (i * kVThreads + tid) * 8 + j);
-    }
-    sum = wave_sum_f64(sum);
-    best = (int)~wave_max_u32(~(uint32_t)best);
   }
-  if ((tid & 63) == 0) {
-    s_sum[w] = sum;
-    s_best[w] = best;
-  }
-  __syncthreads();
-  if (tid == 0) {
-    for (int i = 1; i < kVWaves; ++i) {
-      sum += s_sum[i];
-      best = s_best[i] < best ? s_best[i] : best;
-    }
-    a.part[r * a.nchunk + chunk] = VerifyPart{sum, top, best};
-  }
+  if (lane == 0) a.part[id] = VerifyPart{sum, top, best};
 }
 
 // A row's maximum, lowest argmax and sum from its chunks' records (one wave).
@@ -230,7 +227,7 @@ __device__ __forceinline__ float log_prob(float x, const RowFold& f, double k) {
 }
 
 // The weights of 8 values (p, or what q leaves of it, or p without a token)
-// and their sum; x: the logits.
+// from t on, and their sum; x: the logits.
 template <typename T>
 struct Weights {
   const uint8_t* row;
@@ -262,8 +259,10 @@ enum VerifyMode { kAll, kDecide, kDraw };
 // kAll: a workgroup per (sequence, chunk); kDecide: one per sequence, which
 // also draws unless q is to be subtracted; kDraw: per (sequence, chunk), the
 // draws that kDecide left.
+constexpr int decide_threads(VerifyMode m) { return m == kDraw ? kDrawThreads : kDecideThreads; }
 template <typename T, VerifyMode kMode>
-__global__ __launch_bounds__(kDThreads) void verify_decide_kernel(const VerifyArgs a) {
+__global__ __launch_bounds__(decide_threads(kMode)) void verify_decide_kernel(const VerifyArgs a) {
+  constexpr int kDThreads = decide_threads(kMode), kDWaves = kDThreads / kWave;
   __shared__ int s_last[kDWaves];   // 0: the wave's draft was accepted
   __shared__ RowFold s_fold[kDWaves];
   __shared__ int s_token[kDWaves];
@@ -393,11 +392,18 @@ __global__ __launch_bounds__(kDThreads) void verify_decide_kernel(const VerifyAr
   double* pw = a.part_weight + (int64_t)s * a.nchunk;
   float x[8];
   double y[8];
+  // this thread's first value of a chunk, and the chunk's end (threads behind
+  // the chunk have nothing of it)
+  auto end_of = [&](int c) {
+    const int64_t e = (int64_t)(c + 1) * kVerifyChunk;
+    return e < a.v ? e : a.v;
+  };
+  auto first_of = [&](int c) {
+    return tid < kDrawThreads ? (int64_t)c * kVerifyChunk + tid * 8 : end_of(c);
+  };
   // a chunk's weights, this thread's 8 of them in y; the sum is thread 0's
   auto chunk_weight = [&](int c) {
-    const int64_t c0 = (int64_t)c * a.chunk;
-    const int64_t end = c0 + a.chunk < a.v ? c0 + a.chunk : a.v;
-    double sum = wave_sum_f64(wt.at(c0 + tid * 8, end, x, y));
+    double sum = wave_sum_f64(wt.at(first_of(c), end_of(c), x, y));
     if (lane == 0) s_sum[w] = sum;
     __syncthreads();
     if (tid == 0)
@@ -421,7 +427,7 @@ __global__ __launch_bounds__(kDThreads) void verify_decide_kernel(const VerifyAr
     if (!s_go) return;
   }
   // a token that p loses: its chunk's sum without it
-  const int skip_chunk = wt.skip >= 0 ? (int)(wt.skip / a.chunk) : -1;
+  const int skip_chunk = wt.skip >= 0 ? (int)(wt.skip / kVerifyChunk) : -1;
   double skip_sum = 0.0;
   if (skip_chunk >= 0) skip_sum = chunk_weight(skip_chunk);
 
@@ -479,8 +485,8 @@ __global__ __launch_bounds__(kDThreads) void verify_decide_kernel(const VerifyAr
   }
   // the token: the first whose running sum passes what is left of the target
   const double need = s_need;
-  const int64_t c0 = (int64_t)s_chunk * a.chunk, t = c0 + tid * 8;
-  const double sum = wt.at(t, c0 + a.chunk < a.v ? c0 + a.chunk : a.v, x, y);
+  const int64_t t = first_of(s_chunk);
+  const double sum = wt.at(t, end_of(s_chunk), x, y);
   const double scan = wave_scan_f64(sum);
   if (lane == 63) s_sum[w] = scan;
   __syncthreads();
@@ -521,30 +527,21 @@ __global__ __launch_bounds__(kDThreads) void verify_decide_kernel(const VerifyAr
 template <typename T>
 void enqueue(const VerifyArgs& a, hipStream_t s) {
   const unsigned n = (unsigned)a.nchunk, B = (unsigned)a.B;
-  if (a.rows && a.units == 1)
-    hipLaunchKernelGGL((verify_rows_kernel<T, 1>), dim3((unsigned)a.rows * n), dim3(kVThreads), 0,
-                       s, a);
+  const dim3 rows((unsigned)((a.rows * a.nchunk + kVWaves - 1) / kVWaves));
+  if (a.rows && a.sample)
+    hipLaunchKernelGGL((verify_rows_kernel<T, false>), rows, dim3(kVThreads), 0, s, a);
   else if (a.rows)
-    hipLaunchKernelGGL((verify_rows_kernel<T, 2>), dim3((unsigned)a.rows * n), dim3(kVThreads), 0,
-                       s, a);
+    hipLaunchKernelGGL((verify_rows_kernel<T, true>), rows, dim3(kVThreads), 0, s, a);
   if (a.q && (int64_t)B * n <= 512) {
-    hipLaunchKernelGGL((verify_decide_kernel<T, kAll>), dim3(B * n), dim3(kDThreads), 0, s, a);
+    hipLaunchKernelGGL((verify_decide_kernel<T, kAll>), dim3(B * n), dim3(kDecideThreads), 0, s, a);
     return;
   }
-  hipLaunchKernelGGL((verify_decide_kernel<T, kDecide>), dim3(B), dim3(kDThreads), 0, s, a);
+  hipLaunchKernelGGL((verify_decide_kernel<T, kDecide>), dim3(B), dim3(kDecideThreads), 0, s, a);
   if (a.q)
-    hipLaunchKernelGGL((verify_decide_kernel<T, kDraw>), dim3(B * n), dim3(kDThreads), 0, s, a);
+    hipLaunchKernelGGL((verify_decide_kernel<T, kDraw>), dim3(B * n), dim3(kDrawThreads), 0, s, a);
 }
 
 }  // namespace
-
-// Chunks of 4096 values where they make at least 512 workgroups (two a compute
-// unit), else of 2048, so that short batches still reach most compute units.
-void plan_verify(VerifyArgs& a) {
-  a.units = a.rows * ((a.v + 4095) / 4096) >= 512 ? 2 : 1;
-  a.chunk = (int64_t)a.units * kVThreads * 8;
-  a.nchunk = (int)((a.v + a.chunk - 1) / a.chunk);
-}
 
 hipError_t launch_verify(const VerifyArgs& a, int dtype, hipStream_t s) {
   if (dtype == FH_DTYPE_BF16)
