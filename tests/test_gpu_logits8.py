@@ -123,7 +123,9 @@ def test_logits_one_nan_code_of_E(fh):
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("rows,v,d", [(65, 65600, 144), (130, 65537, 256), (300, 40000, 1104),
-                                      (513, 33001, 384), (257, 65536, 16), (2100, 9000, 400)])
+                                      (513, 33001, 384), (257, 65536, 16), (2100, 9000, 400),
+                                      (20, 30000, 272), (300, 4000, 1040), (90, 20000, 640),
+                                      (1030, 2100, 528), (700, 12000, 160)])
 def test_logits_many_tiles(fh, dtype, rows, v, d):
     # enough tiles for the tiled kernels, cut in every direction
     check(fh, rows, v, d, dtype, extra=16)

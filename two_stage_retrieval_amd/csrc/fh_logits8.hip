@@ -79,6 +79,13 @@ __device__ __forceinline__ v4i chunk(const uint8_t* row, int k, int d) {
   return v4i{0, 0, 0, 0};
 }
 
+typedef __bf16 v4bf __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ v4u bf16_pair(v4f a, v4f b) {
+  return __builtin_bit_cast(v4u, __builtin_shufflevector(__builtin_convertvector(a, v4bf),
+                                                         __builtin_convertvector(b, v4bf), 0, 1, 2,
+                                                         3, 4, 5, 6, 7));
+}
+
 // Column of result i (0 .. 3) of a lane's tile j in a run of 16 NT columns,
 // less i: each store instruction writes 64 bytes in a row (16 columns of
 // fp32, or of two tiles' 32 of bf16).  Result row r = 4 q + i of tile j is
@@ -119,13 +126,11 @@ __device__ __forceinline__ void store_run(const Logits8Args& a, int m, int64_t n
 }
 
 // ---------------------------------------------------------------------------
-// Tiles: kBM rows of h by 256 rows of E per workgroup of 8 waves, each wave
-// kBM / 2 by 64.  Blocks of 128 columns go from memory to LDS without
+// Tiles: kBM rows of h by kBN of E per workgroup of 8 waves, each wave kBM / 2
+// by kBN / 4.  Blocks of 128 columns go from memory to LDS without
 // passing registers (two buffers: the next block's loads run under the
 // present block's products).
 // ---------------------------------------------------------------------------
-constexpr int kBN = 256;
-
 // LDS rows are 128 bytes: eight 16-byte slots.  Chunk k of row r is held in
 // slot k ^ key(r), so that the eight lanes that read one chunk of eight rows
 // at a time touch eight different slots.
@@ -170,10 +175,11 @@ __device__ __forceinline__ void load_lds_wait() {
 // the loads of the next one's first block, so that neither stands alone.
 constexpr int kTileGroups = 256;  // compute units
 
-template <int kBM, bool kExact, typename TO>
+template <int kBM, int kBN, bool kExact, typename TO>
 __global__ __launch_bounds__(512, 2) void logits8_tiles_kernel(const Logits8Args a) {
   constexpr int MT = kBM / 32;   // 16-row tiles of h per wave
-  constexpr int kStores = MT * (sizeof(TO) == 2 ? 2 : 4);   // of a wave's results
+  constexpr int NT = kBN / 64;   // and of E
+  constexpr int kStores = MT * NT / (sizeof(TO) == 2 ? 2 : 1);   // of a wave's results
   __shared__ __align__(128) uint8_t s_e[2][kBN * 128];
   __shared__ __align__(128) uint8_t s_h[2][kBM * 128];
   __shared__ __align__(128) float s_hs[2][kBM];
@@ -275,7 +281,7 @@ __global__ __launch_bounds__(512, 2) void logits8_tiles_kernel(const Logits8Args
 
   // where the lane's operands are in LDS: row and byte of the first chunk (the
   // second is four slots on), and the rows between tiles
-  const int e_row = wn * 64 + run_at<TO, 4>(0, c >> 2) + (c & 3);
+  const int e_row = wn * (kBN / 4) + run_at<TO, NT>(0, c >> 2) + (c & 3);
   const int e_slot = 16 * (q ^ key_e<TO>(e_row));
   const int h_row = wm * (kBM / 2) + c, h_slot = 16 * (q ^ key_h(c));
   // the last block of a row that is not whole: h counts as zero past its end
@@ -288,12 +294,12 @@ __global__ __launch_bounds__(512, 2) void logits8_tiles_kernel(const Logits8Args
     __syncthreads();
   };
 
-  v4f acc[MT][4];
+  v4f acc[MT][NT];
   auto clear = [&]() {
 #pragma unroll
     for (int t = 0; t < MT; ++t)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[t][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int j = 0; j < NT; ++j) acc[t][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
   };
   // Stores the wave's part of the tile at m, n, which ends before the last
   // column.  A row that does not exist goes to an offset past the resource's
@@ -302,7 +308,7 @@ __global__ __launch_bounds__(512, 2) void logits8_tiles_kernel(const Logits8Args
     const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(
         static_cast<uint8_t*>(a.out) + ((int64_t)m * a.ldo + n) * sizeof(TO), 0, 0x7FFFFFFF,
         0x00027000);
-    if constexpr (sizeof(TO) == 2) {
+    if constexpr (sizeof(TO) == 2 && NT == 4) {
       // Eight rows of 128 bytes a store instead of sixteen of 64: lane c of a
       // row's first 8 gives away its second half and takes lane c + 8's
       // first (3 % of the whole at 2048 x 128256 x 2048).
@@ -310,14 +316,8 @@ __global__ __launch_bounds__(512, 2) void logits8_tiles_kernel(const Logits8Args
       const uint32_t lane_off = (uint32_t)((c & 7) * a.ldo + 8 * q + (up ? 32 : 0)) * 2;
 #pragma unroll
       for (int t = 0; t < MT; ++t) {
-        typedef __bf16 v4bf __attribute__((ext_vector_type(4)));
-        v4u y[2], z;
-#pragma unroll
-        for (int j = 0; j < 4; j += 2)
-          y[j / 2] = __builtin_bit_cast(
-              v4u, __builtin_shufflevector(__builtin_convertvector(acc[t][j], v4bf),
-                                           __builtin_convertvector(acc[t][j + 1], v4bf), 0, 1, 2,
-                                           3, 4, 5, 6, 7));
+        const v4u y[2] = {bf16_pair(acc[t][0], acc[t][1]), bf16_pair(acc[t][2], acc[t][3])};
+        v4u z;
 #pragma unroll
         for (int i = 0; i < 4; ++i)  // row_ror:8: the lane 8 on in its row of 16
           z[i] = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(up ? y[0][i] : y[1][i]), 0x128,
@@ -333,16 +333,22 @@ __global__ __launch_bounds__(512, 2) void logits8_tiles_kernel(const Logits8Args
         }
       }
     } else {
-      const uint32_t lane_off = (uint32_t)(c * a.ldo + 4 * q) * 4;
+      constexpr int P = sizeof(TO) == 2 ? 2 : 1;   // tiles per store
+      const uint32_t lane_off = (uint32_t)(c * a.ldo + run_at<TO, NT>(0, q)) * sizeof(TO);
 #pragma unroll
       for (int t = 0; t < MT; ++t) {
         const uint32_t off = m + t * 16 + c < a.rows
-                                 ? lane_off + (uint32_t)(t * 16 * a.ldo) * 4
+                                 ? lane_off + (uint32_t)(t * 16 * a.ldo) * sizeof(TO)
                                  : 0x80000000u;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u, acc[t][j]), rsrc,
-                                                 (int)(off + 64 * j), 0, 0);
+        for (int j = 0; j < NT; j += P) {
+          v4u x;
+          if constexpr (P == 2)
+            x = bf16_pair(acc[t][j], acc[t][j + 1]);
+          else
+            x = __builtin_bit_cast(v4u, acc[t][j]);
+          __builtin_amdgcn_raw_buffer_store_b128(x, rsrc, (int)(off + 64 * (j / P)), 0, 0);
+        }
       }
     }
   };
@@ -350,13 +356,13 @@ __global__ __launch_bounds__(512, 2) void logits8_tiles_kernel(const Logits8Args
   // adds the products of the block in buffer st; true if loads of E were made
   auto block = [&](int st) {
     bool more = false;
-    const float s_e_scale = s_es[st][wn >> 1];
-    Frag<kExact> e[4];
+    const float s_e_scale = s_es[st][wn * (kBN / 4) / 128];
+    Frag<kExact> e[NT];
     const uint8_t* pe = s_e[st] + e_row * 128;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      e[j].set(*reinterpret_cast<const v4i*>(pe + run_at<TO, 4>(j, 0) * 128 + e_slot),
-               *reinterpret_cast<const v4i*>(pe + run_at<TO, 4>(j, 0) * 128 + (e_slot ^ 64)));
+    for (int j = 0; j < NT; ++j)
+      e[j].set(*reinterpret_cast<const v4i*>(pe + run_at<TO, NT>(j, 0) * 128 + e_slot),
+               *reinterpret_cast<const v4i*>(pe + run_at<TO, NT>(j, 0) * 128 + (e_slot ^ 64)));
     const uint8_t* ph = s_h[st] + h_row * 128;
     v4i lo, hi;
     float s;
@@ -371,9 +377,9 @@ __global__ __launch_bounds__(512, 2) void logits8_tiles_kernel(const Logits8Args
 #pragma unroll
       for (int t = 0; t < MT; ++t)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) asm volatile("" : "+v"(acc[t][j]));
+        for (int j = 0; j < NT; ++j) asm volatile("" : "+v"(acc[t][j]));
     };
-    v4f x[4];
+    v4f x[NT];
     float xs = 0.0f;
     auto add = [&](int t, int j) {
 #pragma unroll
@@ -388,19 +394,19 @@ __global__ __launch_bounds__(512, 2) void logits8_tiles_kernel(const Logits8Args
       if (t + 1 < MT) read_h(t + 1);
       // The products of this tile run while the last one's are added, one
       // matrix instruction (32 cycles) to four sums (16).
-      v4f y[4];
+      v4f y[NT];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < NT; ++j) {
         y[j] = mfma128(e[j], h);
         if (t > 0) add(t - 1, j);
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[j] = y[j];
+      for (int j = 0; j < NT; ++j) x[j] = y[j];
       xs = x_scale;
       if constexpr (!kExact) {
         __builtin_amdgcn_sched_group_barrier(0x100, 3, 0);  // LDS reads
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < NT; ++j) {
           __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // matrix instruction
           __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);  // vector instructions
         }
@@ -414,7 +420,7 @@ __global__ __launch_bounds__(512, 2) void logits8_tiles_kernel(const Logits8Args
       }
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) add(MT - 1, j);
+    for (int j = 0; j < NT; ++j) add(MT - 1, j);
     pin();
     return more;
   };
@@ -432,7 +438,7 @@ __global__ __launch_bounds__(512, 2) void logits8_tiles_kernel(const Logits8Args
     int64_t n0;
     place(tile, &m0, &n0);
     const int m1 = m0 + wm * (kBM / 2);
-    const int64_t n1 = n0 + wn * 64;
+    const int64_t n1 = n0 + wn * (kBN / 4);
     clear();
     for (int kb = 0; kb + 1 < G; ++kb) {
       load_h(st ^ 1);
@@ -455,7 +461,7 @@ __global__ __launch_bounds__(512, 2) void logits8_tiles_kernel(const Logits8Args
     } else {  // the last column cuts some stores: value by value
 #pragma unroll
       for (int t = 0; t < MT; ++t)
-        if (m1 + t * 16 + c < a.rows) store_run<TO, 4>(a, m1 + t * 16 + c, n1, q, acc[t]);
+        if (m1 + t * 16 + c < a.rows) store_run<TO, NT>(a, m1 + t * 16 + c, n1, q, acc[t]);
       load_lds_wait<0>();
     }
     __syncthreads();
@@ -565,24 +571,37 @@ void enqueue_rows(const Logits8Args& a, hipStream_t s) {
                      dim3(256), 0, s, a);
 }
 
-template <int kBM, bool kExact, typename TO>
+template <int kBM, int kBN, bool kExact, typename TO>
 void enqueue_tiles(const Logits8Args& a, hipStream_t s) {
-  hipLaunchKernelGGL((logits8_tiles_kernel<kBM, kExact, TO>), dim3(kTileGroups), dim3(512), 0, s,
-                     a);
+  hipLaunchKernelGGL((logits8_tiles_kernel<kBM, kBN, kExact, TO>), dim3(kTileGroups), dim3(512), 0,
+                     s, a);
 }
 
-// Time of a kernel in us: rounds of workgroups, blocks a workgroup walks, and
-// the measured time of a block (tiles: 64, 128, 256 rows of h with the 8-bit
-// instruction 0.8, 1.15, 2.2 us, 64 and 128 rows with the bf16 one 1.3 and
-// 2.4; four waves with 32 rows and 64 of E, two workgroups a compute unit: 3
-// us for four blocks).
+// Estimated times in us.  Tiles: 3 us, and for each round of workgroups and
+// each block of columns the measured time of a block (333 x 5003 x 1104, 64 x
+// 16000 x 2048 and 40 x 20000 x 1024 with each tile; a smaller tile has more
+// workgroups and less to do in each).
+struct TileTime {
+  int bm, bn;
+  double fast, exact;  // with the 8-bit and the bf16 instruction
+};
+constexpr TileTime kTileTimes[] = {{64, 128, 0.59, 0.86},
+                                   {128, 128, 0.78, 1.24},
+                                   {64, 256, 0.84, 1.31},
+                                   {128, 256, 1.11, 1.81},
+                                   {256, 256, 2.2, HUGE_VAL}};
 double rounds(int64_t groups, int at_once) { return (double)((groups + at_once - 1) / at_once); }
-template <typename TO>
-double tiles_time(const Logits8Args& a, int bm, double block) {
-  // (the tiles reach 128 rows of out by 31-bit offsets)
-  if (a.ldo * (int64_t)sizeof(TO) >= 1 << 23) return HUGE_VAL;
-  const int64_t tiles = (int64_t)((a.rows + bm - 1) / bm) * ((a.v + kBN - 1) / kBN);
-  return 2.0 + rounds(tiles, kTileGroups) * ((a.d + 127) / 128) * block;
+double tiles_time(const Logits8Args& a, const TileTime& t, bool exact) {
+  const int64_t tiles = (int64_t)((a.rows + t.bm - 1) / t.bm) * ((a.v + t.bn - 1) / t.bn);
+  return 3.0 + rounds(tiles, kTileGroups) * ((a.d + 127) / 128) * (exact ? t.exact : t.fast);
+}
+// Four waves with 32 rows of h and 64 of E, two workgroups a compute unit: 2 us,
+// 2.2 us for four blocks, and E once at the memory's rate (for 672 x 1424 x
+// 560: 6 us, 8 with the smallest tiles).
+double few_time(const Logits8Args& a) {
+  const int64_t groups = (int64_t)((a.rows + 31) / 32) * ((a.v + 63) / 64);
+  return 2.0 + rounds(groups, 2 * kTileGroups) * (((a.d + 127) / 128 + kSplit - 1) / kSplit) * 2.2 +
+         (double)a.v * a.d / 5.4e6;
 }
 
 template <typename TO>
@@ -600,20 +619,27 @@ void enqueue(const Logits8Args& a, hipStream_t s) {
       enqueue_rows<1, 1, TO>(a, s);
     return;
   }
-  const double few = rounds((int64_t)((a.rows + 31) / 32) * ((a.v + 63) / 64), 2 * kTileGroups) *
-                     (((a.d + 127) / 128 + kSplit - 1) / kSplit) * 3.0;
-  const double t64 = tiles_time<TO>(a, 64, exact ? 1.3 : 0.8);
-  const double t128 = tiles_time<TO>(a, 128, exact ? 2.4 : 1.15);
-  const double t256 = exact ? HUGE_VAL : tiles_time<TO>(a, 256, 2.2);
-  const double best = fmin(fmin(few, t64), fmin(t128, t256));
-  if (best == few)
-    enqueue_rows<2, 4, TO>(a, s);
-  else if (best == t64)
-    enqueue_tiles<64, exact, TO>(a, s);
-  else if (best == t128)
-    enqueue_tiles<128, exact, TO>(a, s);
-  else if constexpr (!exact)
-    enqueue_tiles<256, false, TO>(a, s);
+  double best = few_time(a);
+  int tile = -1;
+  // (the tiles reach 128 rows of out by 31-bit offsets)
+  if (a.ldo * (int64_t)sizeof(TO) < 1 << 23)
+    for (int i = 0; i < 5; ++i) {
+      const double t = tiles_time(a, kTileTimes[i], exact);
+      if (t < best) {
+        best = t;
+        tile = i;
+      }
+    }
+  switch (tile) {
+    case 0: enqueue_tiles<64, 128, exact, TO>(a, s); break;
+    case 1: enqueue_tiles<128, 128, exact, TO>(a, s); break;
+    case 2: enqueue_tiles<64, 256, exact, TO>(a, s); break;
+    case 3: enqueue_tiles<128, 256, exact, TO>(a, s); break;
+    case 4:
+      if constexpr (!exact) enqueue_tiles<256, 256, false, TO>(a, s);
+      break;
+    default: enqueue_rows<2, 4, TO>(a, s);
+  }
 }
 
 }  // namespace
