@@ -339,7 +339,8 @@ int dense_head_static(const void* E, int64_t v, int32_t d, int32_t dtype,
  * allowed.  Rows of x, residual, weight, residual_out and y start at multiples
  * of 16 bytes and are multiples of 16 bytes long; rows of y8 start at
  * multiples of 8 bytes (dtype bf16) or 4 (fp32).  rows < 2^24.  The mean of
- * the squares is an fp32 sum: |t| up to about 1e18.
+ * the squares is an fp32 sum: |t| up to about 1e18.  A row of zeros with eps =
+ * 0, and a row with an infinity or NaN, gives NaN in that row.
  */
 int flashhead_rmsnorm(const void* x, int64_t ldx, const void* residual, int64_t ldr,
                       const void* weight, int64_t rows, int32_t d, int32_t dtype, float eps,
@@ -363,14 +364,14 @@ int flashhead_quantize_fp8(const void* E, int64_t v, int32_t d, int32_t dtype, i
  *   out[m, t] = sum over k of h8[m, k] h_scale[m, k / 128]
  *                             * E8[t, k] E_scale[t / 128, k / 128]
  * with fp32 sums, rounded once to out_dtype.  Codes of the e4m3 NaN make the
- * outputs of their row NaN.  With bf16 outputs and more than 16 rows the products
- * may go through the 8-bit matrix instruction, which drops the bits below 2^-13 of
- * the largest product in each 8 columns (about 5e-5 of a typical result, a
- * fortieth of its rounding to bf16); fp32 outputs never do.
+ * outputs of their row NaN.  With bf16 outputs and more than 16 rows the
+ * products may go through the 8-bit matrix instruction, which drops the bits
+ * below 2^-13 of the largest product in each 8 columns (about 5e-5 of a
+ * typical result, a fortieth of its rounding to bf16); fp32 outputs never do.
  *   h8, h_scale   device, rows x d and rows x ceil(d / 128)
  *   E8, E_scale   device, v x d and ceil(v / 128) x ceil(d / 128)
- *   d             a multiple of 16;  rows <= 65535 * 16;  strides of h8,
- *                 h_scale, E8 and E_scale below 2^22
+ *   d             a multiple of 16;  v <= 2^28;  rows <= 65535 * 16;  strides
+ *                 of h8, h_scale, E8 and E_scale below 2^22
  *   out           device, rows x v, FH_DTYPE_F32 or FH_DTYPE_BF16
  * Rows of h8, E8 and out start at multiples of 16 bytes (v itself may be any
  * size; columns [v, ldo) of out are left as they are).  A row's result does
@@ -428,7 +429,8 @@ int dense_logits_fp8(const uint8_t* h8, int64_t ldh, const float* h_scale, int64
  *                 16-byte aligned, one call in flight per workspace; its
  *                 contents need no initialisation, and one made for more
  *                 sequences or rows serves fewer.
- * FH_ERR_INVALID_ARG for a workspace that is too small.
+ * FH_ERR_INVALID_ARG for a workspace that is too small; FH_ERR_UNSUPPORTED
+ * where rows or B times ceil(v / 2048) reach 2^24, or B reaches 2^23.
  */
 size_t flashhead_verify_workspace_bytes(int32_t B, int64_t rows, int64_t v);
 int flashhead_verify(const void* logits, int64_t rows, int64_t v, int32_t dtype, int64_t ldl,

@@ -76,7 +76,7 @@ def test_logits_refusals(fh):
         assert call(**kw) == inv, kw
     for kw in (dict(dtype=3), dict(d=248), dict(h=P + 8), dict(E=P + 4), dict(out=P + 8),
                dict(hs=P + 2), dict(es=P + 2), dict(ldh=264), dict(lde=264), dict(ldo=300),
-               dict(v=2 ** 31, ldo=2 ** 31), dict(rows=65535 * 16 + 1), dict(ldh=1 << 22),
+               dict(v=2 ** 28 + 8, ldo=2 ** 29), dict(rows=65535 * 16 + 1), dict(ldh=1 << 22),
                dict(lde=1 << 22), dict(lds=1 << 22), dict(ldes=1 << 22)):
         assert call(**kw) == uns, kw
 
@@ -105,7 +105,8 @@ def test_verify_refusals(fh):
     assert call(wsb=n - 1) == inv
     for kw in (dict(dtype=5), dict(z=P + 8), dict(q=P + 8), dict(ws=P + 8), dict(ldl=1004),
                dict(ldq=1001), dict(v=2 ** 31, ldl=2 ** 31, ldq=2 ** 31), dict(rows=1 << 24),
-               dict(B=1 << 24)):
+               dict(B=1 << 24), dict(B=1 << 23), dict(rows=1 << 20, v=65536, ldl=65536, ldq=65536),
+               dict(B=1 << 19, v=65536, ldl=65536, ldq=65536)):
         assert call(**kw) == uns, kw
 
 

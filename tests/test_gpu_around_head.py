@@ -1,0 +1,202 @@
+"""The operators around the head in a run, as a speculative decoding step uses
+them: the norm into 8 bits, the 8-bit logits, the verification of drafted
+tokens; FlashHead drafts them.  Each stage is checked against the float64
+definition on what the stage before gave (tests/around_ref.py)."""
+import numpy as np
+import pytest
+
+from . import around_ref as ref
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module")
+def fh():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from two_stage_retrieval_amd import binding
+    return binding
+
+
+def rand(shape, seed, scale=1.0, dtype=torch.bfloat16):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(*shape, generator=g) * scale).to(dtype).cuda()
+
+
+def starts_of(counts):
+    return torch.tensor(np.concatenate([[0], np.cumsum([n + 1 for n in counts])]),
+                        dtype=torch.int32, device="cuda")
+
+
+@pytest.mark.parametrize("v,d,dtype,counts", [(5003, 1152, torch.bfloat16, [3, 0, 5, 1]),
+                                              (20000, 208, torch.float32, [2, 2, 0, 7, 1, 1]),
+                                              (128256, 2048, torch.bfloat16, [4])])
+def test_norm_logits_and_verification_in_a_run(fh, v, d, dtype, counts):
+    rows, n, B = sum(counts) + len(counts), sum(counts), len(counts)
+    E, w = rand((v, d), 1, 0.05, dtype), rand((d,), 2, 0.1, dtype)
+    head = fh.DenseHeadFP8(E, w, weight_offset=1.0, max_rows=rows + 3, max_sequences=B)
+    ref.check_codes(head.E8, head.E_scale, ref.f64(E), 128, 0)
+    x, r = rand((rows, d), 3, 1.0, dtype), rand((rows, d), 4, 2.0, dtype)
+    ro = torch.empty_like(r)
+    g = torch.Generator().manual_seed(5)
+    q = torch.softmax(torch.randn(n, -(-v // 4) * 4, generator=g).cuda() * 2, 1)[:, :v]
+    drafts = torch.multinomial(q, 1)[:, 0].int() if n else torch.empty(0, dtype=torch.int32,
+                                                                        device="cuda")
+    ua, us = torch.rand(n, generator=g).cuda(), torch.rand(B, generator=g).cuda()
+    z = head.empty_logits(rows)
+    tokens, accepted = head.verify(x, starts_of(counts), drafts, max(counts), residual=r,
+                                   residual_out=ro, logits=z, tau=0.9, draft_probs=q, u_accept=ua,
+                                   u_sample=us)
+    torch.cuda.synchronize()
+    t, y = ref.norm(x, r, w, 1e-6, 1.0)
+    assert np.all(np.abs(ref.f64(ro) - t) <= (ref.U32 + ref.half_step(dtype)) * 1.001 * np.abs(t))
+    ref.check_codes(head.h8[:rows], head.h_scale[:rows], y, 1, ref.NORM_STEPS)
+    part = slice(0, min(v, 5120))
+    want, mag = ref.logits(head.h8[:rows], head.h_scale[:rows], head.E8[part],
+                           head.E_scale[:-(-min(v, 5120) // 128)])
+    ref.check_logits(z[:, part], want, mag, d)
+    tk, ac, _ = ref.verify(ref.f64(z), starts_of(counts).tolist(), drafts.tolist(),
+                           max(counts) + 1, sample=True, tau=float(np.float32(0.9)),
+                           q=ref.f64(q), u_accept=ua.tolist(), u_sample=us.tolist())
+    assert tokens.tolist() == tk.tolist() and accepted.tolist() == ac.tolist()
+
+
+def test_flashhead_drafts_the_dense_head_verifies(fh):
+    # greedy drafts of the two-stage head for each position of a batch, then
+    # the dense 8-bit head accepts those that are its own argmax
+    from two_stage_retrieval_amd import synth
+    head0 = synth.make_head(0)
+    B, k, d = 12, 3, head0.wl.d
+    H = torch.from_numpy(synth.make_hidden(head0, B * (k + 1))).cuda()
+    E = torch.from_numpy(head0.E).cuda()
+    two = fh.FlashHead(E, head0.c2t, torch.from_numpy(head0.C_given).cuda(), max_batch=B * k,
+                       max_p=head0.wl.p)
+    at = [b * (k + 1) + j for b in range(B) for j in range(k)]
+    drafts = two.greedy(H[at], head0.wl.p)
+    dense = fh.DenseHeadFP8(E, None, eps=0.0, max_rows=B * (k + 1), max_sequences=B)
+    z = dense.empty_logits(B * (k + 1))
+    tokens, accepted = dense.verify(H, starts_of([k] * B), drafts, k, logits=z,
+                                    mode=fh.FH_MODE_GREEDY)
+    torch.cuda.synchronize()
+    best = z.argmax(1).view(B, k + 1).tolist()
+    dr = drafts.view(B, k).tolist()
+    taken = 0
+    for b in range(B):
+        a = 0
+        while a < k and dr[b][a] == best[b][a]:
+            a += 1
+        taken += a
+        assert accepted[b].item() == a
+        assert tokens[b].tolist() == dr[b][:a] + [best[b][a]] + [-1] * (k - a)
+    assert 0 < taken                       # the heads do agree on some tokens
+    two.close()
+
+
+def test_first_token_follows_the_target(fh):
+    # drafts from q, verified against p: the first token is distributed as p.
+    # 40000 sequences over 24 tokens; each count within 5 standard deviations
+    # (24 counts: one in 70000 runs of a right kernel would be outside, and the
+    # numbers here are fixed)
+    v, B = 24, 40000
+    rng = np.random.default_rng(11)
+    z = torch.from_numpy(rng.normal(size=v) * 1.5).float().cuda()
+    p = torch.softmax(z.double(), 0).cpu().numpy()
+    q = rng.dirichlet(np.ones(v))
+    drafts = rng.choice(v, size=B, p=q)
+    logits = z.repeat(2 * B, 1).contiguous()
+    qd = torch.from_numpy(q).float().cuda().repeat(B, 1).contiguous()
+    ws = torch.empty(fh.flashhead_verify_workspace_bytes(B, 2 * B, v), dtype=torch.uint8,
+                     device="cuda")
+    out = torch.empty(B, 2, dtype=torch.int32, device="cuda")
+    acc = torch.empty(B, dtype=torch.int32, device="cuda")
+    fh.flashhead_verify(logits, torch.arange(0, 2 * B + 1, 2, dtype=torch.int32, device="cuda"),
+                        torch.from_numpy(drafts).int().cuda(), out, acc, ws, draft_probs=qd,
+                        u_accept=torch.from_numpy(rng.random(B)).float().clamp(max=1 - 2.0 ** -24)
+                        .cuda(),
+                        u_sample=torch.from_numpy(rng.random(B)).float().clamp(max=1 - 2.0 ** -24)
+                        .cuda())
+    n = np.bincount(out[:, 0].cpu().numpy(), minlength=v)
+    assert np.all(np.abs(n - B * p) <= 5 * np.sqrt(B * p * (1 - p)) + 1)
+    # and as often accepted as the two agree
+    a = np.minimum(p, q).sum()
+    assert abs(acc.float().mean().item() - a) <= 5 * np.sqrt(a * (1 - a) / B)
+
+
+def test_run_in_a_graph_matches_eager(fh):
+    counts, v, d = [2, 0, 3], 9000, 512
+    rows, n, B = 8, 5, 3
+    head = fh.DenseHeadFP8(rand((v, d), 21, 0.05), rand((d,), 22, 0.1), max_rows=rows,
+                           max_sequences=B)
+    st = starts_of(counts)
+    x, u = rand((rows, d), 23), torch.zeros(n + B, device="cuda")
+    drafts = torch.zeros(n, dtype=torch.int32, device="cuda")
+    z = head.empty_logits(rows)
+    out = torch.empty(B, 4, dtype=torch.int32, device="cuda")
+    acc = torch.empty(B, dtype=torch.int32, device="cuda")
+
+    def step(xx, dd, uu, o, a):
+        head.verify(xx, st, dd, 3, logits=z, out_tokens=o, out_accepted=a, tau=0.7,
+                    u_accept=uu[:n], u_sample=uu[n:])
+
+    step(x, drafts, u, out, acc)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(x, drafts, u, out, acc)
+    torch.cuda.synchronize()
+    for i in range(5):
+        xi = rand((rows, d), 30 + i)
+        zi = head.logits(xi)
+        di = zi.argmax(1)[torch.tensor([0, 1, 4, 5, 6], device="cuda")].int()
+        ui = torch.rand(n + B, generator=torch.Generator().manual_seed(i)).cuda()
+        x.copy_(xi)
+        drafts.copy_(di)
+        u.copy_(ui)
+        g.replay()
+        torch.cuda.synchronize()
+        got = out.clone(), acc.clone()
+        want = torch.empty_like(out), torch.empty_like(acc)
+        step(xi, di, ui, *want)
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_two_heads_on_two_streams(fh):
+    # calls at once, each with its own buffers
+    v, d, rows = 30000, 1024, 24
+    heads = [fh.DenseHeadFP8(rand((v, d), 40 + i, 0.05), max_rows=rows, max_sequences=8)
+             for i in range(2)]
+    x = [rand((rows, d), 50 + i) for i in range(2)]
+    st = torch.arange(0, rows + 1, 3, dtype=torch.int32, device="cuda")
+    u = torch.rand(rows, generator=torch.Generator().manual_seed(1)).cuda()
+    z = [h.empty_logits(rows) for h in heads]
+    drafts = torch.arange(16, dtype=torch.int32, device="cuda")
+    outs = [[torch.empty(8, 3, dtype=torch.int32, device="cuda") for _ in range(2)]
+            for _ in range(2)]
+    accs = [torch.empty(8, dtype=torch.int32, device="cuda") for _ in range(2)]
+    for i in range(2):
+        heads[i].verify(x[i], st, drafts, 2, logits=z[i], out_tokens=outs[0][i],
+                        out_accepted=accs[i], u_accept=u[:16], u_sample=u[16:])
+    torch.cuda.synchronize()
+    want = [z[i].clone() for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(10):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                heads[i].verify(x[i], st, drafts, 2, logits=z[i], out_tokens=outs[1][i],
+                                out_accepted=accs[i], u_accept=u[:16], u_sample=u[16:])
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert torch.equal(z[i], want[i]) and torch.equal(outs[0][i], outs[1][i])
+
+
+def test_more_rows_than_made_for(fh):
+    head = fh.DenseHeadFP8(rand((512, 256), 60, 0.05), max_rows=4, max_sequences=2)
+    with pytest.raises(ValueError):
+        head.logits(rand((5, 256), 61))
+    with pytest.raises(fh.FlashHeadError):      # three sequences: the workspace is too small
+        z = rand((4, 256), 62)
+        head.verify(z, torch.tensor([0, 1, 2, 4], dtype=torch.int32, device="cuda"),
+                    torch.zeros(1, dtype=torch.int32, device="cuda"), 1,
+                    u_accept=torch.zeros(1, device="cuda"), u_sample=torch.zeros(3, device="cuda"))

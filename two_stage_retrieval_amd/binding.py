@@ -675,3 +675,72 @@ class DenseHead:
         dense_head(self.E, H, B, mode, tau, seeds, out, out_lse, self.ws,
                    stream=stream)
         return out
+
+
+class DenseHeadFP8:
+    """The dense head in 8 bits behind its norm: the final norm's output goes
+    straight into 8 bits, E is held as e4m3 codes with their scales (E itself
+    is not kept), and drafted tokens are verified against the logits.
+
+    max_rows, max_sequences: largest calls; the 8-bit rows and the
+    verification's workspace are made for them once, so one call is in flight
+    per object."""
+
+    def __init__(self, E, norm_weight=None, *, eps: float = 1e-6, weight_offset: float = 0.0,
+                 max_rows: int = 64, max_sequences: int = 64, logits_dtype=None, stream=None):
+        torch = _torch()
+        self.v, self.d = E.shape
+        if self.d % 16:
+            raise ValueError("a width that is a multiple of 16 is expected")
+        self.eps, self.weight_offset, self.norm_weight = eps, weight_offset, norm_weight
+        self.logits_dtype = E.dtype if logits_dtype is None else logits_dtype
+        g, dev = -(-self.d // FH_FP8_BLOCK), E.device
+        f8 = torch.float8_e4m3fn
+        self.E8 = torch.empty(self.v, self.d, dtype=f8, device=dev)
+        self.E_scale = torch.empty(-(-self.v // FH_FP8_BLOCK), g, device=dev)
+        flashhead_quantize_fp8(E, self.E8, self.E_scale, stream)
+        self.h8 = torch.empty(max_rows, self.d, dtype=f8, device=dev)
+        self.h_scale = torch.empty(max_rows, g, device=dev)
+        self.workspace = torch.empty(
+            flashhead_verify_workspace_bytes(max_sequences, max_rows, self.v),
+            dtype=torch.uint8, device=dev)
+
+    def empty_logits(self, rows: int):
+        """rows x v whose rows start at multiples of 16 bytes, as the calls take them."""
+        torch = _torch()
+        per = 16 // torch.empty(0, dtype=self.logits_dtype).element_size()
+        return torch.empty(rows, -(-self.v // per) * per, dtype=self.logits_dtype,
+                           device=self.E8.device)[:, :self.v]
+
+    def logits(self, x, residual=None, residual_out=None, out=None, stream=None):
+        """Logits of the norm of the rows of x (+ residual)."""
+        rows = x.shape[0]
+        if rows > self.h8.shape[0]:
+            raise ValueError("more rows than the head was made for")
+        if out is None:
+            out = self.empty_logits(rows)
+        h8, h_scale = self.h8[:rows], self.h_scale[:rows]
+        flashhead_rmsnorm(x, self.norm_weight, residual=residual, residual_out=residual_out,
+                          y8=h8, y_scale=h_scale, eps=self.eps,
+                          weight_offset=self.weight_offset, stream=stream)
+        dense_logits_fp8(h8, h_scale, self.E8, self.E_scale, out, stream)
+        return out
+
+    def verify(self, x, row_start, draft_tokens, max_drafts: int, *, residual=None,
+               residual_out=None, logits=None, out_tokens=None, out_accepted=None, stream=None,
+               **how):
+        """The tokens of each sequence (B x (max_drafts + 1): accepted drafts,
+        the next token, then -1) and the number of accepted drafts, from the
+        hidden rows x of the drafted positions and the one after them.  `how`:
+        mode, tau, draft_probs, u_accept, u_sample, out_logp of
+        flashhead_verify; logits: where to put them."""
+        torch = _torch()
+        B = row_start.numel() - 1
+        if out_tokens is None:
+            out_tokens = torch.empty(B, max_drafts + 1, dtype=torch.int32, device=x.device)
+        if out_accepted is None:
+            out_accepted = torch.empty(B, dtype=torch.int32, device=x.device)
+        z = self.logits(x, residual, residual_out, logits, stream)
+        flashhead_verify(z, row_start, draft_tokens, out_tokens, out_accepted, self.workspace,
+                         stream=stream, **how)
+        return out_tokens, out_accepted

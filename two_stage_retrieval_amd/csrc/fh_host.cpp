@@ -188,7 +188,7 @@ int check_logits_fp8(const void* h8, int64_t ldh, const void* h_scale, int64_t l
                      int32_t d, const void* out, int32_t out_dtype, int64_t ldo) {
   if (rows < 0 || v < 1 || d < 1 || !E8 || !E_scale) return FH_ERR_INVALID_ARG;
   if (rows > 0 && (!h8 || !h_scale || !out)) return FH_ERR_INVALID_ARG;
-  if (v > (int64_t)INT32_MAX || rows > 65535 * 16) return FH_ERR_UNSUPPORTED;
+  if (v > (int64_t)1 << 28 || rows > 65535 * 16) return FH_ERR_UNSUPPORTED;
   const int es = esize_of(out_dtype);
   if (!es || d % 16) return FH_ERR_UNSUPPORTED;
   const int32_t groups = (d + 127) / 128;
@@ -228,9 +228,10 @@ int check_verify(const void* logits, int64_t rows, int64_t v, int32_t dtype, int
   if (st == FH_OK) st = check_rows16(draft_probs, ldq, v, 4, n_drafts);
   if (st != FH_OK) return st;
   if (!aligned16(workspace)) return FH_ERR_UNSUPPORTED;
-  // a chunk has at least 2048 values
+  // chunks of 2048 values; 512 threads a sequence
   const int64_t chunks = (v + 2047) / 2048;
-  if (rows > kMaxGroups / chunks || B > kMaxGroups / chunks) return FH_ERR_UNSUPPORTED;
+  if (rows > kMaxGroups / chunks || B > kMaxGroups / chunks || B > kMaxGroups / 2)
+    return FH_ERR_UNSUPPORTED;
   return FH_OK;
 }
 
