@@ -884,6 +884,7 @@ int flashhead_rmsnorm(const void* x, int64_t ldx, const void* residual, int64_t 
   a.r = static_cast<const uint8_t*>(residual);
   a.r_bytes = ldr * es;
   a.w = static_cast<const uint8_t*>(weight);
+  a.rows = rows;
   a.d = d;
   a.units = d * es / 16;
   a.eps = eps;
@@ -896,7 +897,7 @@ int flashhead_rmsnorm(const void* x, int64_t ldx, const void* residual, int64_t 
   a.ldy8 = ldy8;
   a.scale = y_scale;
   a.lds = lds;
-  FH_TRY(launch_rmsnorm(a, dtype, rows, static_cast<hipStream_t>(stream)));
+  FH_TRY(launch_rmsnorm(a, dtype, static_cast<hipStream_t>(stream)));
   return FH_OK;
 }
 

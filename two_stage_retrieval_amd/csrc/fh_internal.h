@@ -328,6 +328,7 @@ struct RmsnormArgs {
   const uint8_t* r;      // residual, or null
   int64_t r_bytes;
   const uint8_t* w;      // weight, or null (ones)
+  int64_t rows;
   int d, units;          // columns; 16-byte chunks per row
   float eps, offset;
   uint8_t* r_out;        // x + r, or null
@@ -339,7 +340,7 @@ struct RmsnormArgs {
   float* scale;          // rows x ceil(d / 128), with y8
   int64_t lds;
 };
-hipError_t launch_rmsnorm(const RmsnormArgs& a, int dtype, int64_t rows, hipStream_t s);
+hipError_t launch_rmsnorm(const RmsnormArgs& a, int dtype, hipStream_t s);
 struct QuantizeFp8Args {
   const uint8_t* E;
   int64_t e_bytes;

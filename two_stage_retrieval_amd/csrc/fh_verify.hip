@@ -20,9 +20,10 @@
 // chunk's running sum the token.  Only max(p - q, 0) has other chunk sums than
 // p: then a workgroup per chunk sums the chunk's weights, and the sequence's
 // last one draws.  Those decide for themselves in the second launch where
-// they all fit the device at once (one sequence of four drafts, 128256: 19 us
-// in two launches); where they do not (64 sequences: 41 us, mostly the same
-// decisions made 32 times over), a third launch takes over the second's state.
+// they all fit the device at once (one sequence of four drafts, 128256: 5 + 8
+// us); where they do not, a third launch takes over the second's state (64
+// sequences: 32 + 9 + 16 us; with the same decisions made by every chunk's
+// workgroup the second launch took 41).
 #include "fh_device.h"
 #include "fh_internal.h"
 
@@ -63,8 +64,9 @@ __device__ __forceinline__ double wave_sum_f64(double x) { return lane_f64(wave_
 // nearest whole number, it is 2^f with n added to the exponent; n is the low
 // word of y + 1.5 * 2^52, and 2^f the polynomial that interpolates it at the
 // ten Chebyshev nodes of [-1/2, 1/2] (relative error below 2e-14).  These
-// instructions set the time of the first launch: 288 rows of 128256 took 80 us
-// with the library's exp and 42 with the conversions to and from n.
+// instructions set the time of the first launch (21 fp64 ones a value, 5 cycles
+// each on average): 288 rows of 128256 take 32 us, where reading them takes 14;
+// 80 with the library's exp, 42 with conversions to and from n.
 template <bool kZero = true>
 __device__ __forceinline__ double weight(float x, float top, double k) {
   double y = ((double)x - (double)top) * k;
