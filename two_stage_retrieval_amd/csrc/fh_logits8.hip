@@ -127,9 +127,9 @@ __device__ __forceinline__ void store_run(const Logits8Args& a, int m, int64_t n
 
 // ---------------------------------------------------------------------------
 // Tiles: kBM rows of h by kBN of E per workgroup of 8 waves, each wave kBM / 2
-// by kBN / 4.  Blocks of 128 columns go from memory to LDS without
-// passing registers (two buffers: the next block's loads run under the
-// present block's products).
+// by kBN / 4.  Blocks of 128 columns go from memory to LDS without passing
+// registers (two buffers: the next block's loads run under the present block's
+// products).
 // ---------------------------------------------------------------------------
 // LDS rows are 128 bytes: eight 16-byte slots.  Chunk k of row r is held in
 // slot k ^ key(r), so that the eight lanes that read one chunk of eight rows
@@ -162,7 +162,8 @@ __device__ __forceinline__ void load_lds4(const void* base, uint32_t off, uint32
                : "s"(lds), "v"(off), "s"(base)
                : "memory", "m0");
 }
-// waits until at most n of the wave's later memory operations are open
+// Waits until at most n of the wave's memory operations, the last ones, are
+// open (they end in the order in which they were issued, stores among them).
 template <int n>
 __device__ __forceinline__ void load_lds_wait() {
   asm volatile("s_waitcnt vmcnt(%0)" : : "i"(n) : "memory");
@@ -247,7 +248,7 @@ __global__ __launch_bounds__(512, 2) void logits8_tiles_kernel(const Logits8Args
     s_off = w == 7 ? (two ? (uint32_t)a.ldes * 4 : 0u)
                    : (uint32_t)min(tid, h_last) * (uint32_t)a.lds * 4;
   };
-  // kELoads, kHLoads + 1 at most, of a wave; false when there is no more
+  // kELoads of a wave; false when there is no more
   constexpr int kELoads = kBN / 64;
   auto load_e = [&](int st) {
     if (e_tile >= last) return false;
@@ -411,8 +412,9 @@ __global__ __launch_bounds__(512, 2) void logits8_tiles_kernel(const Logits8Args
       xs = x_scale;
       // (reads stay one tile ahead: all at once they would not fit the registers)
       __builtin_amdgcn_sched_barrier(0);
-      if (t == (MT > 2 ? 1 : 0)) {  // E's operands are in every wave's registers
-        __builtin_amdgcn_s_barrier();
+      if (t == (MT > 2 ? 1 : 0)) {
+        // E's operands are in every wave's registers: the buffer is free
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
         more = load_e(st);
         pin();
       }
