@@ -191,6 +191,37 @@ def test_two_heads_on_two_streams(fh):
         assert torch.equal(z[i], want[i]) and torch.equal(outs[0][i], outs[1][i])
 
 
+def test_tensors_made_for_a_given_stream(fh):
+    # The logits of a call on another stream must not lie where work that is
+    # still queued on the current one writes.
+    v, d, rows = 30000, 512, 24
+    E, x = rand((v, d), 70, 0.05), rand((rows, d), 71)
+    side = torch.cuda.Stream()
+    head = fh.DenseHeadFP8(E, max_rows=rows, max_sequences=8)
+    want = head.logits(x).clone()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        junk = head.empty_logits(rows)
+        torch.cuda._sleep(20_000_000)           # some ms, then the write
+        junk.fill_(float("nan"))
+        del junk
+        z = head.logits(x, stream=side.cuda_stream)
+        torch.cuda.synchronize()
+        assert torch.equal(z, want)
+        del z
+    st = torch.arange(0, rows + 1, 3, dtype=torch.int32, device="cuda")
+    u = torch.rand(rows, generator=torch.Generator().manual_seed(2)).cuda()
+    drafts = torch.arange(16, dtype=torch.int32, device="cuda")
+    a = head.verify(x, st, drafts, 2, u_accept=u[:16], u_sample=u[16:])
+    torch.cuda.synchronize()
+    other = torch.cuda.Stream()
+    made = fh.DenseHeadFP8(E, max_rows=rows, max_sequences=8, stream=other.cuda_stream)
+    b = made.verify(x, st, drafts, 2, u_accept=u[:16], u_sample=u[16:],
+                    stream=other.cuda_stream)
+    torch.cuda.synchronize()
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
 def test_more_rows_than_made_for(fh):
     head = fh.DenseHeadFP8(rand((512, 256), 60, 0.05), max_rows=4, max_sequences=2)
     with pytest.raises(ValueError):

@@ -7,6 +7,7 @@ import of this module fails loudly; there is no fallback path.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import os
 from typing import Optional
@@ -676,6 +677,14 @@ class DenseHead:
                    stream=stream)
         return out
 
+def _made_on(stream):
+    """For tensors that work on `stream` (a raw handle) uses first: torch's
+    allocator hands memory on in the order of the stream it was made on."""
+    if stream is None:
+        return contextlib.nullcontext()
+    torch = _torch()
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream))
+
 
 class DenseHeadFP8:
     """The dense head in 8 bits behind its norm: the final norm's output goes
@@ -684,7 +693,7 @@ class DenseHeadFP8:
 
     max_rows, max_sequences: largest calls; the 8-bit rows and the
     verification's workspace are made for them once, so one call is in flight
-    per object."""
+    per object.  Tensors that a call makes belong to its stream."""
 
     def __init__(self, E, norm_weight=None, *, eps: float = 1e-6, weight_offset: float = 0.0,
                  max_rows: int = 64, max_sequences: int = 64, logits_dtype=None, stream=None):
@@ -696,14 +705,15 @@ class DenseHeadFP8:
         self.logits_dtype = E.dtype if logits_dtype is None else logits_dtype
         g, dev = -(-self.d // FH_FP8_BLOCK), E.device
         f8 = torch.float8_e4m3fn
-        self.E8 = torch.empty(self.v, self.d, dtype=f8, device=dev)
-        self.E_scale = torch.empty(-(-self.v // FH_FP8_BLOCK), g, device=dev)
+        with _made_on(stream):
+            self.E8 = torch.empty(self.v, self.d, dtype=f8, device=dev)
+            self.E_scale = torch.empty(-(-self.v // FH_FP8_BLOCK), g, device=dev)
+            self.h8 = torch.empty(max_rows, self.d, dtype=f8, device=dev)
+            self.h_scale = torch.empty(max_rows, g, device=dev)
+            self.workspace = torch.empty(
+                flashhead_verify_workspace_bytes(max_sequences, max_rows, self.v),
+                dtype=torch.uint8, device=dev)
         flashhead_quantize_fp8(E, self.E8, self.E_scale, stream)
-        self.h8 = torch.empty(max_rows, self.d, dtype=f8, device=dev)
-        self.h_scale = torch.empty(max_rows, g, device=dev)
-        self.workspace = torch.empty(
-            flashhead_verify_workspace_bytes(max_sequences, max_rows, self.v),
-            dtype=torch.uint8, device=dev)
 
     def empty_logits(self, rows: int):
         """rows x v whose rows start at multiples of 16 bytes, as the calls take them."""
@@ -718,7 +728,8 @@ class DenseHeadFP8:
         if rows > self.h8.shape[0]:
             raise ValueError("more rows than the head was made for")
         if out is None:
-            out = self.empty_logits(rows)
+            with _made_on(stream):
+                out = self.empty_logits(rows)
         h8, h_scale = self.h8[:rows], self.h_scale[:rows]
         flashhead_rmsnorm(x, self.norm_weight, residual=residual, residual_out=residual_out,
                           y8=h8, y_scale=h_scale, eps=self.eps,
@@ -736,10 +747,11 @@ class DenseHeadFP8:
         flashhead_verify; logits: where to put them."""
         torch = _torch()
         B = row_start.numel() - 1
-        if out_tokens is None:
-            out_tokens = torch.empty(B, max_drafts + 1, dtype=torch.int32, device=x.device)
-        if out_accepted is None:
-            out_accepted = torch.empty(B, dtype=torch.int32, device=x.device)
+        with _made_on(stream):
+            if out_tokens is None:
+                out_tokens = torch.empty(B, max_drafts + 1, dtype=torch.int32, device=x.device)
+            if out_accepted is None:
+                out_accepted = torch.empty(B, dtype=torch.int32, device=x.device)
         z = self.logits(x, residual, residual_out, logits, stream)
         flashhead_verify(z, row_start, draft_tokens, out_tokens, out_accepted, self.workspace,
                          stream=stream, **how)
