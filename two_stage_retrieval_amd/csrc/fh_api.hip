@@ -975,6 +975,7 @@ int flashhead_verify(const void* logits, int64_t rows, int64_t v, int32_t dtype,
   a.ldq = ldq;
   a.sample = mode == FH_MODE_SAMPLE;
   a.k = 1.4426950408889634074 / (a.sample ? (double)tau : 1.0);
+  a.lo = -1020.0 / a.k;
   a.u_accept = u_accept;
   a.u_sample = u_sample;
   a.max_tokens = max_tokens;

@@ -395,7 +395,7 @@ struct VerifyArgs {
   const float* q;            // n_drafts x v probabilities, or null (one-hot)
   int64_t ldq;
   int sample;
-  double k;                  // log2(e) / tau (tau 1 for greedy decoding)
+  double k, lo;              // log2(e) / tau (tau 1 for greedy decoding); -1020 / k
   const float* u_accept;
   const float* u_sample;
   int max_tokens;

@@ -212,7 +212,7 @@ void enqueue_rmsnorm(const RmsnormArgs& a, hipStream_t s) {
     hipLaunchKernelGGL((rmsnorm_kernel<T, kNormThreads, 2>), each, block, 0, s, a);
   else if (a.units <= 4 * kNormThreads)
     hipLaunchKernelGGL((rmsnorm_kernel<T, kNormThreads, 4>), each, block, 0, s, a);
-  else
+  else if constexpr (sizeof(T) == 4)
     hipLaunchKernelGGL((rmsnorm_kernel<T, kNormThreads, 8>), each, block, 0, s, a);
 }
 

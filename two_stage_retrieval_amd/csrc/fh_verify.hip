@@ -22,7 +22,7 @@
 // last one draws.  Those decide for themselves in the second launch where
 // they all fit the device at once (one sequence of four drafts, 128256: 5 + 8
 // us); where they do not, a third launch takes over the second's state (64
-// sequences: 32 + 9 + 16 us; with the same decisions made by every chunk's
+// sequences: 31 + 9 + 16 us; with the same decisions made by every chunk's
 // workgroup the second launch took 41).
 #include "fh_device.h"
 #include "fh_internal.h"
@@ -60,18 +60,19 @@ __device__ __forceinline__ double lane_f64(double x, int lane) {
 __device__ __forceinline__ double wave_sum_f64(double x) { return lane_f64(wave_scan_f64(x), 63); }
 
 // 2^((x - top) k) for x <= top, not NaN; kZero: 0 from 2^-1020 on, else at
-// least about that (enough for a sum that holds a 1).  With y = n + f, n the
-// nearest whole number, it is 2^f with n added to the exponent; n is the low
-// word of y + 1.5 * 2^52, and 2^f the polynomial that interpolates it at the
-// ten Chebyshev nodes of [-1/2, 1/2] (relative error below 2e-14).  These
-// instructions set the time of the first launch (21 fp64 ones a value, 5 cycles
-// each on average): 288 rows of 128256 take 32 us, where reading them takes 14;
-// 80 with the library's exp, 42 with conversions to and from n.
+// least about that (enough for a sum that holds a 1; lo = -1020 / k).  With
+// (x - top) k = n + f, n the nearest whole number, it is 2^f with n added to the
+// exponent; n is the low word of a sum with 1.5 * 2^52, and 2^f the polynomial
+// that interpolates it at the ten Chebyshev nodes of [-1/2, 1/2] (relative error
+// below 2e-14).  These instructions set the time of the first launch: 17 a
+// value, about 1 us each for 288 rows of 128256, which take 31 us in all where
+// reading them takes 14 (80 with the library's exp, 42 with conversions to and
+// from n; requesting the next values before these are summed changes nothing).
 template <bool kZero = true>
-__device__ __forceinline__ double weight(float x, float top, double k) {
-  double y = ((double)x - (double)top) * k;
-  if constexpr (!kZero) y = fmax(y, -1020.0);
-  const double n = y + 6755399441055744.0, f = y - (n - 6755399441055744.0);
+__device__ __forceinline__ double weight(float x, float top, double k, double lo = 0.0) {
+  double d = (double)x - (double)top;
+  if constexpr (!kZero) d = fmax(d, lo);
+  const double n = fma(d, k, 6755399441055744.0), f = fma(d, k, 6755399441055744.0 - n);
   double p = 1.02059054137655955e-07;
   p = fma(p, f, 1.32596452448871106e-06);
   p = fma(p, f, 1.52526729248507372e-05);
@@ -83,7 +84,7 @@ __device__ __forceinline__ double weight(float x, float top, double k) {
   p = fma(p, f, 6.93147180559946174e-01);
   p = fma(p, f, 1.00000000000001354e+00);
   p = __hiloint2double(__double2hiint(p) + (__double2loint(n) << 20), __double2loint(p));
-  if constexpr (kZero) p = y < -1020.0 ? 0.0 : p;
+  if constexpr (kZero) p = n < 6755399441055744.0 - 1020.0 ? 0.0 : p;
   return p;
 }
 
@@ -176,7 +177,7 @@ __global__ __launch_bounds__(kVThreads) void verify_rows_kernel(const VerifyArgs
 #pragma unroll
     for (int i = 0; i < U; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) part[j & 1] += weight<false>(x[i][j], top, a.k);
+      for (int j = 0; j < 8; ++j) part[j & 1] += weight<false>(x[i][j], top, a.k, a.lo);
     sum = wave_sum_f64(part[0] + part[1]);
     if constexpr (kBest) {
 #pragma unroll
