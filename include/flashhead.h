@@ -363,11 +363,8 @@ int flashhead_quantize_fp8(const void* E, int64_t v, int32_t d, int32_t dtype, i
  * codes stand for):
  *   out[m, t] = sum over k of h8[m, k] h_scale[m, k / 128]
  *                             * E8[t, k] E_scale[t / 128, k / 128]
- * with fp32 sums, rounded once to out_dtype.  Codes of the e4m3 NaN make the
- * outputs of their row NaN.  With bf16 outputs and more than 16 rows the
- * products may go through the 8-bit matrix instruction, which drops the bits
- * below 2^-13 of the largest product in each 8 columns (about 5e-5 of a
- * typical result, a fortieth of its rounding to bf16); fp32 outputs never do.
+ * with exact products of two codes and fp32 sums, rounded once to out_dtype.
+ * Codes of the e4m3 NaN make the outputs of their row NaN.
  *   h8, h_scale   device, rows x d and rows x ceil(d / 128)
  *   E8, E_scale   device, v x d and ceil(v / 128) x ceil(d / 128)
  *   d             a multiple of 16;  v <= 2^28;  rows <= 65535 * 16;  strides
@@ -375,8 +372,8 @@ int flashhead_quantize_fp8(const void* E, int64_t v, int32_t d, int32_t dtype, i
  *   out           device, rows x v, FH_DTYPE_F32 or FH_DTYPE_BF16
  * Rows of h8, E8 and out start at multiples of 16 bytes (v itself may be any
  * size; columns [v, ldo) of out are left as they are).  A row's result does
- * not depend on the other rows' values, and a call is reproducible bit for
- * bit.
+ * not depend on the other rows' values (their number may change the order of
+ * its fp32 sums), and a call is reproducible bit for bit.
  */
 int dense_logits_fp8(const uint8_t* h8, int64_t ldh, const float* h_scale, int64_t lds,
                      int32_t rows, const uint8_t* E8, int64_t lde, const float* E_scale,

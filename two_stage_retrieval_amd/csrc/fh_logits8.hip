@@ -4,8 +4,6 @@
 // 128 x 128 block of E.  The products of a block of 128 columns are summed by
 // the matrix cores; its fp32 result is then scaled and added to the fp32
 // accumulator, since the scales change from block to block.
-#include <math.h>
-
 #include "fh_device.h"
 #include "fh_internal.h"
 
@@ -13,7 +11,6 @@ namespace fh {
 
 namespace {
 
-typedef int v8i __attribute__((ext_vector_type(8)));
 typedef int v4i __attribute__((ext_vector_type(4)));
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 typedef float v4f __attribute__((ext_vector_type(4)));
@@ -30,20 +27,16 @@ __device__ __forceinline__ v8bf to_bf16(int w0, int w1) {
   return v8bf{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-// A lane's 32 bytes of a 16-row operand's block, as the matrix instructions
-// take them: lane l gives bytes of row l % 16 (any order of the columns that
-// both operands share).
+// A lane's 32 bytes of a 16-row operand's block, as bf16 values, as the matrix
+// instruction takes them: lane l gives bytes of row l % 16 (any order of the
+// columns that both operands share).
 //
-// kExact: as bf16 values, for the bf16 instruction.  Otherwise the codes, for
-// the 8-bit instruction, which runs at twice the rate but cuts products short:
-// within each group of 8 it drops the bits below 2^-13 of the group's largest
-// product (measured; 4.5e-5 of the result on codes spread over the whole
-// format, against 3e-8 for the bf16 instruction).  That is a fortieth of
-// what rounding a result to bf16 costs, so it serves bf16 outputs only, and
-// only from 17 rows of h on, where it is faster (32 x 128256 x 2048: 41 us, 51
-// with the bf16 instruction).
-template <bool kExact> struct Frag;
-template <> struct Frag<true> {
+// The 8-bit matrix instruction would take the codes themselves at twice the
+// rate, but cuts products short: within each group of 8 it drops the bits below
+// 2^-13 of the group's largest product (measured; 4.5e-5 of the result on codes
+// spread over the whole format, against 3e-8 for the bf16 instruction).  The
+// sums are held to 32 bits here, for every number of rows and type of output.
+struct Frag {
   v8bf x[4];
   __device__ __forceinline__ void set(v4i lo, v4i hi) {
     x[0] = to_bf16(lo[0], lo[1]);
@@ -52,25 +45,15 @@ template <> struct Frag<true> {
     x[3] = to_bf16(hi[2], hi[3]);
   }
 };
-template <> struct Frag<false> {
-  v8i x;
-  __device__ __forceinline__ void set(v4i lo, v4i hi) {
-    x = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-  }
-};
 
 // D[i, j] = sum over a block's columns of A[i, :] . B[j, :]; lane l receives
 // rows 4 (l / 16) + 0..3 of column l % 16
-__device__ __forceinline__ v4f mfma128(const Frag<true>& a, const Frag<true>& b) {
+__device__ __forceinline__ v4f mfma128(const Frag& a, const Frag& b) {
   v4f c = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.x[i], b.x[i], c, 0, 0, 0);
   return c;
-}
-__device__ __forceinline__ v4f mfma128(const Frag<false>& a, const Frag<false>& b) {
-  const v4f zero = {0.0f, 0.0f, 0.0f, 0.0f};
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a.x, b.x, zero, 0, 0, 0, 0, 0, 0);
 }
 
 // 16 bytes of a row at column k, zero past its end (d is a multiple of 16)
@@ -175,14 +158,13 @@ __device__ __forceinline__ void load_lds_wait() {
 // ahead.  This goes on over the ends of tiles, and a tile's stores are behind
 // the loads of the next one's first block, so that neither stands alone.
 //
-// 2048 x 128256 x 2048 to bf16 takes 560 to 600 us (1.8 to 1.9 PFLOP/s; a
-// library's 8-bit product of these sizes, without the scales, 541).  The matrix
-// instructions fill 245 us at 2.1 GHz; without loads and stores the kernel takes
-// 356 (the sums and LDS reads between them), loads add about 90 us and stores 80
-// (they wait in the same order as the next loads).
+// 2048 x 128256 x 2048 to bf16 takes 1054 us (1.02 PFLOP/s; a library's bf16
+// product of these sizes, without the scales and with E already in bf16, 943).
+// The matrix instructions fill 489 us at 2.1 GHz; between them are the
+// conversions of both operands, the LDS reads and the sums.
 constexpr int kTileGroups = 256;  // compute units
 
-template <int kBM, int kBN, bool kExact, typename TO>
+template <int kBM, int kBN, typename TO>
 __global__ __launch_bounds__(512, 2) void logits8_tiles_kernel(const Logits8Args a) {
   constexpr int MT = kBM / 32;   // 16-row tiles of h per wave
   constexpr int NT = kBN / 64;   // and of E
@@ -318,7 +300,7 @@ __global__ __launch_bounds__(512, 2) void logits8_tiles_kernel(const Logits8Args
     if constexpr (sizeof(TO) == 2 && NT == 4) {
       // Eight rows of 128 bytes a store instead of sixteen of 64: lane c of a
       // row's first 8 gives away its second half and takes lane c + 8's
-      // first (3 % of the whole at 2048 x 128256 x 2048).
+      // first (16 us less at 2048 x 128256 x 2048).
       const bool up = c >= 8;
       const uint32_t lane_off = (uint32_t)((c & 7) * a.ldo + 8 * q + (up ? 32 : 0)) * 2;
 #pragma unroll
@@ -364,7 +346,7 @@ __global__ __launch_bounds__(512, 2) void logits8_tiles_kernel(const Logits8Args
   auto block = [&](int st) {
     bool more = false;
     const float s_e_scale = s_es[st][wn * (kBN / 4) / 128];
-    Frag<kExact> e[NT];
+    Frag e[NT];
     const uint8_t* pe = s_e[st] + e_row * 128;
 #pragma unroll
     for (int j = 0; j < NT; ++j)
@@ -395,12 +377,12 @@ __global__ __launch_bounds__(512, 2) void logits8_tiles_kernel(const Logits8Args
     read_h(0);
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
-      Frag<kExact> h;
+      Frag h;
       h.set(lo, hi);
       const float x_scale = s * s_e_scale;
       if (t + 1 < MT) read_h(t + 1);
-      // The products of this tile run while the last one's are added, one
-      // matrix instruction (32 cycles) to four sums (16).
+      // The products of this tile run while the last one's are added, four
+      // matrix instructions (64 cycles) to four sums (16).
       v4f y[NT];
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
@@ -523,7 +505,7 @@ __global__ __launch_bounds__(256, 2) void logits8_rows_kernel(const Logits8Args 
   int kb = w;
   if (kb < G) load(kb);
   for (; kb < G; kb += kSplit) {
-    Frag<true> ef[NT], hf[MT];
+    Frag ef[NT], hf[MT];
     float sc[MT];
 #pragma unroll
     for (int j = 0; j < NT; ++j) ef[j].set(re[j].lo, re[j].hi);
@@ -573,10 +555,9 @@ void enqueue_rows(const Logits8Args& a, hipStream_t s) {
                      dim3(256), 0, s, a);
 }
 
-template <int kBM, int kBN, bool kExact, typename TO>
+template <int kBM, int kBN, typename TO>
 void enqueue_tiles(const Logits8Args& a, hipStream_t s) {
-  hipLaunchKernelGGL((logits8_tiles_kernel<kBM, kBN, kExact, TO>), dim3(kTileGroups), dim3(512), 0,
-                     s, a);
+  hipLaunchKernelGGL((logits8_tiles_kernel<kBM, kBN, TO>), dim3(kTileGroups), dim3(512), 0, s, a);
 }
 
 // Estimated times in us.  Tiles: 3 us, and for each round of workgroups and
@@ -585,17 +566,14 @@ void enqueue_tiles(const Logits8Args& a, hipStream_t s) {
 // workgroups and less to do in each).
 struct TileTime {
   int bm, bn;
-  double fast, exact;  // with the 8-bit and the bf16 instruction
+  double block;
 };
-constexpr TileTime kTileTimes[] = {{64, 128, 0.59, 0.86},
-                                   {128, 128, 0.78, 1.24},
-                                   {64, 256, 0.84, 1.31},
-                                   {128, 256, 1.11, 1.81},
-                                   {256, 256, 2.2, HUGE_VAL}};
+constexpr TileTime kTileTimes[] = {
+    {64, 128, 0.86}, {128, 128, 1.24}, {64, 256, 1.31}, {128, 256, 1.81}};
 double rounds(int64_t groups, int at_once) { return (double)((groups + at_once - 1) / at_once); }
-double tiles_time(const Logits8Args& a, const TileTime& t, bool exact) {
+double tiles_time(const Logits8Args& a, const TileTime& t) {
   const int64_t tiles = (int64_t)((a.rows + t.bm - 1) / t.bm) * ((a.v + t.bn - 1) / t.bn);
-  return 3.0 + rounds(tiles, kTileGroups) * ((a.d + 127) / 128) * (exact ? t.exact : t.fast);
+  return 3.0 + rounds(tiles, kTileGroups) * ((a.d + 127) / 128) * t.block;
 }
 // Four waves with 32 rows of h and 64 of E, two workgroups a compute unit: 2 us,
 // 2.2 us for four blocks, and E once at the memory's rate (for 672 x 1424 x
@@ -608,7 +586,6 @@ double few_time(const Logits8Args& a) {
 
 template <typename TO>
 void enqueue(const Logits8Args& a, hipStream_t s) {
-  constexpr bool exact = sizeof(TO) == 4;
   if (a.rows <= 16) {
     // As many rows of E a workgroup as leave most compute units one (1 x 4000
     // x 4096: 7 us with 16, 9 with 32; 16 x 32000 x 2048: 14 us with 64, 21
@@ -625,21 +602,18 @@ void enqueue(const Logits8Args& a, hipStream_t s) {
   int tile = -1;
   // (the tiles reach 128 rows of out by 31-bit offsets)
   if (a.ldo * (int64_t)sizeof(TO) < 1 << 23)
-    for (int i = 0; i < 5; ++i) {
-      const double t = tiles_time(a, kTileTimes[i], exact);
+    for (int i = 0; i < 4; ++i) {
+      const double t = tiles_time(a, kTileTimes[i]);
       if (t < best) {
         best = t;
         tile = i;
       }
     }
   switch (tile) {
-    case 0: enqueue_tiles<64, 128, exact, TO>(a, s); break;
-    case 1: enqueue_tiles<128, 128, exact, TO>(a, s); break;
-    case 2: enqueue_tiles<64, 256, exact, TO>(a, s); break;
-    case 3: enqueue_tiles<128, 256, exact, TO>(a, s); break;
-    case 4:
-      if constexpr (!exact) enqueue_tiles<256, 256, false, TO>(a, s);
-      break;
+    case 0: enqueue_tiles<64, 128, TO>(a, s); break;
+    case 1: enqueue_tiles<128, 128, TO>(a, s); break;
+    case 2: enqueue_tiles<64, 256, TO>(a, s); break;
+    case 3: enqueue_tiles<128, 256, TO>(a, s); break;
     default: enqueue_rows<2, 4, TO>(a, s);
   }
 }
