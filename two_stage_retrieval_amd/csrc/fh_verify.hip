@@ -62,27 +62,30 @@ __device__ __forceinline__ double wave_sum_f64(double x) { return lane_f64(wave_
 // 2^((x - top) k) for x <= top, not NaN; kZero: 0 from 2^-1020 on, else at
 // least about that (enough for a sum that holds a 1; lo = -1020 / k).  With
 // (x - top) k = n + f, n the nearest whole number, it is 2^f with n added to the
-// exponent; n is the low word of a sum with 1.5 * 2^52, and 2^f the polynomial
-// that interpolates it at the ten Chebyshev nodes of [-1/2, 1/2] (relative error
-// below 2e-14).  These instructions set the time of the first launch: 17 a
-// value, about 1 us each for 288 rows of 128256, which take 31 us in all where
-// reading them takes 14 (80 with the library's exp, 42 with conversions to and
-// from n; requesting the next values before these are summed changes nothing).
+// exponent; n is the low word of a sum with 1.5 * 2^52, and 2^f is 1 + f r(f), r
+// the polynomial that interpolates (2^f - 1) / f at the nine Chebyshev nodes of
+// [-1/2, 1/2] (relative error below 4e-14).  The weight of the largest value is
+// 1 itself, so that the running sums over equal largest values are whole numbers
+// and a uniform number on a border between two of them falls on the right side.
+// These instructions set the time of the first launch: 17 a value, about 1 us
+// each for 288 rows of 128256, which take 31 us in all where reading them takes
+// 14 (80 with the library's exp, 42 with conversions to and from n; requesting
+// the next values before these are summed changes nothing).
 template <bool kZero = true>
 __device__ __forceinline__ double weight(float x, float top, double k, double lo = 0.0) {
   double d = (double)x - (double)top;
   if constexpr (!kZero) d = fmax(d, lo);
   const double n = fma(d, k, 6755399441055744.0), f = fma(d, k, 6755399441055744.0 - n);
-  double p = 1.02059054137655955e-07;
-  p = fma(p, f, 1.32596452448871106e-06);
-  p = fma(p, f, 1.52526729248507372e-05);
-  p = fma(p, f, 1.54034337512510097e-04);
-  p = fma(p, f, 1.33335582007945925e-03);
-  p = fma(p, f, 9.61812919393431262e-03);
-  p = fma(p, f, 5.55041086646516704e-02);
-  p = fma(p, f, 2.40226506956403407e-01);
-  p = fma(p, f, 6.93147180559946174e-01);
-  p = fma(p, f, 1.00000000000001354e+00);
+  double p = 1.02031210633917290e-07;
+  p = fma(p, f, 1.32552248786688168e-06);
+  p = fma(p, f, 1.52526868462677196e-05);
+  p = fma(p, f, 1.54034558524538382e-04);
+  p = fma(p, f, 1.33335581790431116e-03);
+  p = fma(p, f, 9.61812915940255843e-03);
+  p = fma(p, f, 5.55041086647604237e-02);
+  p = fma(p, f, 2.40226506958129887e-01);
+  p = fma(p, f, 6.93147180559945286e-01);
+  p = fma(p, f, 1.0);
   p = __hiloint2double(__double2hiint(p) + (__double2loint(n) << 20), __double2loint(p));
   if constexpr (kZero) p = n < 6755399441055744.0 - 1020.0 ? 0.0 : p;
   return p;
