@@ -384,9 +384,13 @@ int dense_logits_fp8(const uint8_t* h8, int64_t ldh, const float* h_scale, int64
  * Verification of drafted tokens (speculative decoding) for B sequences.
  * Sequence s has the logits' rows row_start[s] .. row_start[s + 1] - 1: one
  * for each of its n drafted tokens and one after them, so n = row_start[s + 1]
- * - row_start[s] - 1 may be 0.  Its j-th draft is entry row_start[s] - s + j
- * of draft_tokens, draft_probs and u_accept (the drafts of all sequences one
- * after the other).  With p_j = softmax(logits / tau) at its row,
+ * - row_start[s] - 1 may be 0.  A slot without a row (row_start[s + 1] ==
+ * row_start[s]) holds no sequence and may be anywhere in the batch.  The
+ * drafts of all sequences are one after the other in draft_tokens, draft_probs
+ * and u_accept: the j-th of sequence s is entry row_start[s] - (sequences
+ * before s that have a row) + j.  (Arrays too short to hold them so are read as
+ * if every slot before s had a row.)  With p_j = softmax(logits / tau) at its
+ * row,
  *   sample   draft x_j is accepted while u_accept[j] q_j(x_j) < p_j(x_j),
  *            q_j its row of draft_probs, or 1 at x_j and 0 elsewhere when
  *            draft_probs is NULL (a draft chosen without chance).  At the

@@ -614,6 +614,7 @@ size_t verify_layout(VerifyArgs& a, uint8_t* base) {
   a.part_weight = reinterpret_cast<double*>(take(seqs * chunks * sizeof(double)));
   a.arrived = reinterpret_cast<uint32_t*>(take(seqs * sizeof(uint32_t)));
   a.state = reinterpret_cast<VerifyState*>(take(seqs * sizeof(VerifyState)));
+  a.empty = reinterpret_cast<int32_t*>(take(seqs * sizeof(int32_t)));
   return at;
 }
 

@@ -407,6 +407,7 @@ struct VerifyArgs {
   VerifyPart* part;          // rows x nchunk
   double* part_weight;       // B x nchunk
   uint32_t* arrived;         // B
+  int32_t* empty;            // B: sequences before it without a row
   VerifyState* state;        // B
   int B;
 };

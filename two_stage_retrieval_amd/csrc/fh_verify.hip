@@ -133,11 +133,42 @@ __device__ __forceinline__ float load1(const uint8_t* row, int64_t i) {
     return reinterpret_cast<const float*>(row)[i];
 }
 
+// a.empty[s] = the sequences before s that have no row and so take none of the
+// places that rows without a draft have (one workgroup, a quarter of the
+// sequences a wave); 0 where the arrays are too short for the drafts of all
+// sequences one after the other.
+__device__ __forceinline__ void count_empty(const VerifyArgs& a, int w, int lane) {
+  __shared__ int s_count[kVWaves];
+  const int64_t per = ((a.B + kVWaves - 1) / kVWaves + kWave - 1) / kWave * kWave;
+  const int64_t from = w * per < a.B ? w * per : a.B;
+  const int64_t to = from + per < a.B ? from + per : a.B;
+  auto none = [&](int64_t s) { return s < to && a.row_start[s + 1] <= a.row_start[s]; };
+  int count = 0;
+#pragma unroll 4
+  for (int64_t s = from; s < to; s += kWave) count += __builtin_popcountll(__ballot(none(s + lane)));
+  if (lane == 0) s_count[w] = count;
+  __syncthreads();
+  int before = 0, total = 0;
+  for (int i = 0; i < kVWaves; ++i) {
+    before += i < w ? s_count[i] : 0;
+    total += s_count[i];
+  }
+  const bool whole = a.n_drafts >= (int64_t)a.row_start[a.B] - (a.B - total);
+  for (int64_t s = from; s < to; s += kWave) {
+    const uint64_t m = __ballot(none(s + lane));
+    if (s + lane < to)
+      a.empty[s + lane] =
+          whole ? before + __builtin_popcountll(m & ((1ull << lane) - 1)) : 0;
+    before += __builtin_popcountll(m);
+  }
+}
+
 // The record of a (row, chunk), one wave each: top = the maximum, best = its
 // lowest index (kBest; greedy decoding), sum = the sum of exp((z - top) / tau).
 // A NaN or +inf logit makes the sum NaN; a chunk of -inf alone has sum 0.
 // A lane holds 32 values, so that the wave's reductions are a tenth of the
-// work, and no wave waits for another.
+// work, and no wave waits for another.  The first workgroup counts the empty
+// sequences instead.
 template <typename T, bool kBest>
 __global__ __launch_bounds__(kVThreads) void verify_rows_kernel(const VerifyArgs a) {
   constexpr int U = kVerifyChunk / (kWave * 8);
@@ -146,7 +177,12 @@ __global__ __launch_bounds__(kVThreads) void verify_rows_kernel(const VerifyArgs
   for (int64_t s = (int64_t)blockIdx.x * kVThreads + tid; s < a.B;
        s += (int64_t)gridDim.x * kVThreads)
     a.arrived[s] = 0u;
-  const int64_t id = (int64_t)blockIdx.x * kVWaves + __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int w = __builtin_amdgcn_readfirstlane(tid / kWave);
+  if (blockIdx.x == 0) {
+    count_empty(a, w, lane);
+    return;
+  }
+  const int64_t id = (int64_t)(blockIdx.x - 1) * kVWaves + w;
   const int64_t r = id / a.nchunk;
   if (r >= a.rows) return;
   const uint8_t* row = a.logits + r * a.l_bytes;
@@ -297,7 +333,7 @@ __global__ __launch_bounds__(decide_threads(kMode)) void verify_decide_kernel(co
   } else {
     const bool writer = chunk == 0;
     const int64_t r0 = a.row_start[s], r1 = a.row_start[s + 1];
-    const int64_t d0 = r0 - s;         // the sequence's first draft
+    const int64_t d0 = r0 - s + a.empty[s];  // the sequence's first draft
     const int64_t n = r1 - r0 - 1;     // its drafts
     bool bad = r0 < 0 || n < 0 || r1 > a.rows || n >= a.max_tokens || d0 < 0 ||
                d0 + n > a.n_drafts;
@@ -533,7 +569,7 @@ __global__ __launch_bounds__(decide_threads(kMode)) void verify_decide_kernel(co
 template <typename T>
 void enqueue(const VerifyArgs& a, hipStream_t s) {
   const unsigned n = (unsigned)a.nchunk, B = (unsigned)a.B;
-  const dim3 rows((unsigned)((a.rows * a.nchunk + kVWaves - 1) / kVWaves));
+  const dim3 rows((unsigned)((a.rows * a.nchunk + kVWaves - 1) / kVWaves) + 1);
   if (a.rows && a.sample)
     hipLaunchKernelGGL((verify_rows_kernel<T, false>), rows, dim3(kVThreads), 0, s, a);
   else if (a.rows)
