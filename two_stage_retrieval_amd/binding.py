@@ -677,13 +677,21 @@ class DenseHead:
                    stream=stream)
         return out
 
+
+def _torch_stream(stream: int):
+    """torch's stream of a raw handle on the current device.  The default
+    stream's is 0, which torch's constructor takes for none given: it would
+    return one of its own."""
+    torch = _torch()
+    return torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+
+
 def _made_on(stream):
     """For tensors that work on `stream` (a raw handle) uses first: torch's
     allocator hands memory on in the order of the stream it was made on."""
     if stream is None:
         return contextlib.nullcontext()
-    torch = _torch()
-    return torch.cuda.stream(torch.cuda.ExternalStream(stream))
+    return _torch().cuda.stream(_torch_stream(stream))
 
 
 class DenseHeadFP8:
