@@ -701,7 +701,10 @@ class DenseHeadFP8:
 
     max_rows, max_sequences: largest calls; the 8-bit rows and the
     verification's workspace are made for them once, so one call is in flight
-    per object.  Tensors that a call makes belong to its stream."""
+    per object.  Tensors that a call makes belong to its stream; a call on
+    another stream than the object's waits for nothing by itself.  An object may
+    be dropped while its calls are queued, on whichever streams, and E once the
+    object is made (a graph's replays need the object, as any tensor of theirs)."""
 
     def __init__(self, E, norm_weight=None, *, eps: float = 1e-6, weight_offset: float = 0.0,
                  max_rows: int = 64, max_sequences: int = 64, logits_dtype=None, stream=None):
@@ -722,6 +725,22 @@ class DenseHeadFP8:
                 flashhead_verify_workspace_bytes(max_sequences, max_rows, self.v),
                 dtype=torch.uint8, device=dev)
         flashhead_quantize_fp8(E, self.E8, self.E_scale, stream)
+        self._streams = set()
+        self._use(stream)
+        if stream is not None:
+            E.record_stream(_torch_stream(stream))
+
+    def _use(self, stream):
+        """The allocator hands the object's memory on when every stream of its
+        calls is done with it (told once for each stream)."""
+        raw = _kinds().stream(self.E8.get_device()) if stream is None else stream
+        if raw not in self._streams:
+            used = _torch_stream(raw)
+            for t in (self.E8, self.E_scale, self.h8, self.h_scale, self.workspace,
+                      self.norm_weight):
+                if t is not None and t.is_cuda:
+                    t.record_stream(used)
+            self._streams.add(raw)
 
     def empty_logits(self, rows: int):
         """rows x v whose rows start at multiples of 16 bytes, as the calls take them."""
@@ -735,6 +754,7 @@ class DenseHeadFP8:
         rows = x.shape[0]
         if rows > self.h8.shape[0]:
             raise ValueError("more rows than the head was made for")
+        self._use(stream)
         if out is None:
             with _made_on(stream):
                 out = self.empty_logits(rows)
