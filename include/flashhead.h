@@ -338,9 +338,11 @@ int dense_head_static(const void* E, int64_t v, int32_t d, int32_t dtype,
  * residual themselves (the same address and stride); no other overlap is
  * allowed.  Rows of x, residual, weight, residual_out and y start at multiples
  * of 16 bytes and are multiples of 16 bytes long; rows of y8 start at
- * multiples of 8 bytes (dtype bf16) or 4 (fp32).  rows < 2^24.  The mean of
- * the squares is an fp32 sum: |t| up to about 1e18.  A row of zeros with eps =
- * 0, and a row with an infinity or NaN, gives NaN in that row.
+ * multiples of 8 bytes (dtype bf16) or 4 (fp32).  rows < 2^24.  Values may be of
+ * any size: the mean of the squares is an fp32 sum, taken again in fp64 where
+ * that is below 2^-100 or past the range of fp32.  A row of zeros with eps = 0
+ * is NaN, and so is a row with a NaN; an infinity is NaN itself and makes the
+ * row's other values zero.
  */
 int flashhead_rmsnorm(const void* x, int64_t ldx, const void* residual, int64_t ldr,
                       const void* weight, int64_t rows, int32_t d, int32_t dtype, float eps,

@@ -74,6 +74,10 @@ __device__ __forceinline__ void store_codes(uint8_t* p, const float* q) {
     *reinterpret_cast<uint32_t*>(p) = e4m3x4(q[0], q[1], q[2], q[3]);
 }
 
+// From this mean of squares on, with eps, the roundings of squares and sums below
+// 2^-126 (by up to 2^-150 each) are nothing beside a row's sum.
+constexpr float kSmallMean = 7.88860905e-31f;  // 2^-100
+
 // kRowThreads threads per row (a wave, four rows a workgroup, or the whole
 // workgroup); the row stays in registers between the sum and the outputs, so x
 // may be y and r may be the residual's output.  Bound by memory: 8192 rows of
@@ -117,14 +121,47 @@ __global__ __launch_bounds__(kNormThreads) void rmsnorm_kernel(const RmsnormArgs
 #pragma unroll
     for (int w = 0; w < kNormThreads / kWave; ++w) tot += s_sum[w];
   }
-  const float rstd = 1.0f / sqrtf(tot / (float)a.d + a.eps);
+  const float mean = tot / (float)a.d + a.eps;
+  float rstd = 1.0f / sqrtf(mean);
+  const bool wide = !(mean >= kSmallMean && mean < INFINITY);
+  if (wide) {
+    // The squares leave the range of fp32: the same in fp64, where they do not.
+    // Also 1 / sqrt(mean) may be out of range where t times it is not.
+    __shared__ double s_wide[kNormThreads / kWave];
+    double sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        sum = fma((double)t[i][j], (double)t[i][j], sum);
+        asm volatile("" : "+v"(t[i][j]));  // (not kept in fp64 for the loop below)
+      }
+    }
+    for (int o = kWave / 2; o > 0; o >>= 1) sum += __shfl_xor(sum, o, kWave);
+    if constexpr (kRows == 1) {  // (the mean, and so this branch, is the workgroup's)
+      if ((tid & (kWave - 1)) == 0) s_wide[tid / kWave] = sum;
+      __syncthreads();
+      sum = 0.0;
+      for (int w = 0; w < kNormThreads / kWave; ++w) sum += s_wide[w];
+    }
+    const double r = 1.0 / sqrt(sum / (double)a.d + (double)a.eps);
+    rstd = 1.0f;
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+      const int u = i * kRowThreads + tid;
+      if (a.r_out && u < a.units)
+        Unit<T>::store(a.r_out + row * a.ro_bytes + (int64_t)u * 16, t[i]);
+#pragma unroll
+      for (int j = 0; j < N; ++j) t[i][j] = (float)((double)t[i][j] * r);
+    }
+  }
 #pragma unroll
   for (int i = 0; i < kUnits; ++i) {
     const int u = i * kRowThreads + tid;
     const bool in = u < a.units;
     float y[N];
     if (in) {
-      if (a.r_out) Unit<T>::store(a.r_out + row * a.ro_bytes + (int64_t)u * 16, t[i]);
+      if (a.r_out && !wide) Unit<T>::store(a.r_out + row * a.ro_bytes + (int64_t)u * 16, t[i]);
       float w[N];
       if (a.w) Unit<T>::load(a.w + (int64_t)u * 16, w);
 #pragma unroll
