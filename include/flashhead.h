@@ -314,7 +314,8 @@ int dense_head_static(const void* E, int64_t v, int32_t d, int32_t dtype,
  * at the matrix's ends), has one fp32 scale max(max|y| / 448, 2^-126); a code
  * is the e4m3 of y / scale, to nearest, ties to even, and stands for code *
  * scale.  Strides are in elements and need at least the columns of a row;
- * with one row a stride is not looked at.  Zero rows (or sequences) are
+ * with one row a stride is not looked at, and one that puts rows past 64-bit
+ * addresses is FH_ERR_UNSUPPORTED.  Zero rows (or sequences) are
  * allowed and do nothing.  Unlike the other calls these take matrices of any
  * number of rows.
  */
@@ -433,7 +434,8 @@ int dense_logits_fp8(const uint8_t* h8, int64_t ldh, const float* h_scale, int64
  *                 contents need no initialisation, and one made for more
  *                 sequences or rows serves fewer.
  * FH_ERR_INVALID_ARG for a workspace that is too small; FH_ERR_UNSUPPORTED
- * where rows or B times ceil(v / 2048) reach 2^24, or B reaches 2^23.
+ * where rows or B times ceil(v / 2048) reach 2^24 - 1, or B reaches 2^23
+ * (workspace_bytes is 0 for sizes that the call refuses).
  */
 size_t flashhead_verify_workspace_bytes(int32_t B, int64_t rows, int64_t v);
 int flashhead_verify(const void* logits, int64_t rows, int64_t v, int32_t dtype, int64_t ldl,

@@ -881,9 +881,9 @@ int flashhead_rmsnorm(const void* x, int64_t ldx, const void* residual, int64_t 
   const int es = esize_of(dtype);
   RmsnormArgs a{};
   a.x = static_cast<const uint8_t*>(x);
-  a.x_bytes = ldx * es;
+  a.x_bytes = row_stride(x, ldx, rows) * es;
   a.r = static_cast<const uint8_t*>(residual);
-  a.r_bytes = ldr * es;
+  a.r_bytes = row_stride(residual, ldr, rows) * es;
   a.w = static_cast<const uint8_t*>(weight);
   a.rows = rows;
   a.d = d;
@@ -891,13 +891,13 @@ int flashhead_rmsnorm(const void* x, int64_t ldx, const void* residual, int64_t 
   a.eps = eps;
   a.offset = weight_offset;
   a.r_out = static_cast<uint8_t*>(residual_out);
-  a.ro_bytes = ldro * es;
+  a.ro_bytes = row_stride(residual_out, ldro, rows) * es;
   a.y = static_cast<uint8_t*>(y);
-  a.y_bytes = ldy * es;
+  a.y_bytes = row_stride(y, ldy, rows) * es;
   a.y8 = y8;
-  a.ldy8 = ldy8;
+  a.ldy8 = row_stride(y8, ldy8, rows);
   a.scale = y_scale;
-  a.lds = lds;
+  a.lds = row_stride(y_scale, lds, rows);
   FH_TRY(launch_rmsnorm(a, dtype, static_cast<hipStream_t>(stream)));
   return FH_OK;
 }
@@ -908,13 +908,13 @@ int flashhead_quantize_fp8(const void* E, int64_t v, int32_t d, int32_t dtype, i
   if (st != FH_OK) return st;
   QuantizeFp8Args a{};
   a.E = static_cast<const uint8_t*>(E);
-  a.e_bytes = lde * esize_of(dtype);
+  a.e_bytes = row_stride(E, lde, v) * esize_of(dtype);
   a.v = v;
   a.d = d;
   a.codes = E8;
-  a.ldc = lde8;
+  a.ldc = row_stride(E8, lde8, v);
   a.scale = E_scale;
-  a.lds = lds;
+  a.lds = row_stride(E_scale, lds, (v + 127) / 128);
   FH_TRY(launch_quantize_fp8(a, dtype, static_cast<hipStream_t>(stream)));
   return FH_OK;
 }
@@ -927,26 +927,25 @@ int dense_logits_fp8(const uint8_t* h8, int64_t ldh, const float* h_scale, int64
                                   out_dtype, ldo);
   if (st != FH_OK || rows == 0) return st;
   Logits8Args a{};
-  // (strides that no second row uses may hold anything)
   a.h8 = h8;
-  a.ldh = rows > 1 ? ldh : d;
+  a.ldh = row_stride(h8, ldh, rows);
   a.h_scale = h_scale;
-  a.lds = rows > 1 ? lds : 0;
+  a.lds = row_stride(h_scale, lds, rows);
   a.rows = rows;
   a.E8 = E8;
-  a.lde = v > 1 ? lde : d;
+  a.lde = row_stride(E8, lde, v);
   a.E_scale = E_scale;
-  a.ldes = v > 128 ? ldes : 0;
+  a.ldes = row_stride(E_scale, ldes, (v + 127) / 128);
   a.v = v;
   a.d = d;
   a.out = out;
-  a.ldo = ldo;
+  a.ldo = row_stride(out, ldo, rows);
   FH_TRY(launch_logits8(a, out_dtype, static_cast<hipStream_t>(stream)));
   return FH_OK;
 }
 
 size_t flashhead_verify_workspace_bytes(int32_t B, int64_t rows, int64_t v) {
-  if (B < 0 || rows < 0 || v < 1 || v > (int64_t)INT32_MAX) return 0;
+  if (B < 0 || rows < 0 || v < 1 || v > (int64_t)INT32_MAX || !verify_fits(rows, B, v)) return 0;
   VerifyArgs a{};
   a.rows = rows;
   a.v = v;
@@ -966,14 +965,14 @@ int flashhead_verify(const void* logits, int64_t rows, int64_t v, int32_t dtype,
   if (st != FH_OK || B == 0) return st;
   VerifyArgs a{};
   a.logits = static_cast<const uint8_t*>(logits);
-  a.l_bytes = ldl * esize_of(dtype);
+  a.l_bytes = row_stride(logits, ldl, rows) * esize_of(dtype);
   a.rows = rows;
   a.v = v;
   a.row_start = row_start;
   a.draft_tokens = draft_tokens;
   a.n_drafts = n_drafts;
   a.q = draft_probs;
-  a.ldq = ldq;
+  a.ldq = row_stride(draft_probs, ldq, n_drafts);
   a.sample = mode == FH_MODE_SAMPLE;
   a.k = 1.4426950408889634074 / (a.sample ? (double)tau : 1.0);
   a.lo = -1020.0 / a.k;

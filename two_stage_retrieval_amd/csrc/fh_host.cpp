@@ -131,15 +131,21 @@ constexpr int64_t kMaxGroups = ((int64_t)1 << 24) - 1;
 
 bool aligned(const void* p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
 
+// rows `ld` elements of `es` bytes apart that no address space holds
+bool too_far(int64_t ld, int es, int64_t rows) { return rows > 1 && ld > INT64_MAX / es / rows; }
+
 // an optional matrix of `es`-byte elements whose rows start at multiples of 16 bytes
 int check_rows16(const void* p, int64_t ld, int64_t cols, int es, int64_t rows) {
   if (!p) return FH_OK;
   if (rows > 1 && ld < cols) return FH_ERR_INVALID_ARG;
-  if (!aligned16(p) || (rows > 1 && (ld * es) % 16)) return FH_ERR_UNSUPPORTED;
+  if (!aligned16(p) || (rows > 1 && ld % (16 / es)) || too_far(ld, es, rows))
+    return FH_ERR_UNSUPPORTED;
   return FH_OK;
 }
 
 }  // namespace
+
+int64_t row_stride(const void* p, int64_t ld, int64_t rows) { return p && rows > 1 ? ld : 0; }
 
 int check_rmsnorm(const void* x, int64_t ldx, const void* residual, int64_t ldr,
                   const void* weight, int64_t rows, int32_t d, int32_t dtype, float eps,
@@ -162,7 +168,8 @@ int check_rmsnorm(const void* x, int64_t ldx, const void* residual, int64_t ldr,
   if (y8) {
     const int n = 16 / es;  // codes a thread stores at once
     if (rows > 1 && (ldy8 < d || lds < (d + 127) / 128)) return FH_ERR_INVALID_ARG;
-    if (!aligned(y8, (uintptr_t)n) || (rows > 1 && ldy8 % n) || !aligned(y_scale, 4))
+    if (!aligned(y8, (uintptr_t)n) || (rows > 1 && ldy8 % n) || !aligned(y_scale, 4) ||
+        too_far(ldy8, 1, rows) || too_far(lds, 4, rows))
       return FH_ERR_UNSUPPORTED;
   }
   return FH_OK;
@@ -178,7 +185,8 @@ int check_quantize_fp8(const void* E, int64_t v, int32_t d, int32_t dtype, int64
   if (v > 1 && lde8 < d) return FH_ERR_INVALID_ARG;
   if (v > 128 && lds < (d + 127) / 128) return FH_ERR_INVALID_ARG;
   const int n = 16 / es;
-  if (!aligned(E8, (uintptr_t)n) || (v > 1 && lde8 % n) || !aligned(E_scale, 4))
+  if (!aligned(E8, (uintptr_t)n) || (v > 1 && lde8 % n) || !aligned(E_scale, 4) ||
+      too_far(lde8, 1, v) || too_far(lds, 4, (v + 127) / 128))
     return FH_ERR_UNSUPPORTED;
   return FH_OK;
 }
@@ -206,6 +214,12 @@ int check_logits_fp8(const void* h8, int64_t ldh, const void* h_scale, int64_t l
   return FH_OK;
 }
 
+bool verify_fits(int64_t rows, int32_t B, int64_t v) {
+  // chunks of 2048 values; 512 threads a sequence
+  const int64_t chunks = (v + 2047) / 2048;
+  return rows <= kMaxGroups / chunks && B <= kMaxGroups / chunks && B <= kMaxGroups / 2;
+}
+
 int check_verify(const void* logits, int64_t rows, int64_t v, int32_t dtype, int64_t ldl,
                  const void* row_start, int32_t B, const void* draft_tokens, int64_t n_drafts,
                  const void* draft_probs, int64_t ldq, int32_t mode, float tau,
@@ -228,11 +242,7 @@ int check_verify(const void* logits, int64_t rows, int64_t v, int32_t dtype, int
   if (st == FH_OK) st = check_rows16(draft_probs, ldq, v, 4, n_drafts);
   if (st != FH_OK) return st;
   if (!aligned16(workspace)) return FH_ERR_UNSUPPORTED;
-  // chunks of 2048 values; 512 threads a sequence
-  const int64_t chunks = (v + 2047) / 2048;
-  if (rows > kMaxGroups / chunks || B > kMaxGroups / chunks || B > kMaxGroups / 2)
-    return FH_ERR_UNSUPPORTED;
-  return FH_OK;
+  return verify_fits(rows, B, v) ? FH_OK : FH_ERR_UNSUPPORTED;
 }
 
 }  // namespace fh

@@ -49,6 +49,10 @@ void quantize_int4(const uint16_t* C, const double* shift, int c, int d,
                    std::vector<uint8_t>& codes, std::vector<uint16_t>& scales, int* ntiles_out,
                    int* groups_out);
 
+// The row stride that a call uses of an optional matrix: 0 where no second row
+// is there (such a stride may hold anything).
+int64_t row_stride(const void* p, int64_t ld, int64_t rows);
+
 // The argument checks of the calls around the 8-bit head (see
 // include/flashhead.h for what each call accepts): FH_OK, or the status the
 // call returns before it touches the device.
@@ -61,6 +65,7 @@ int check_quantize_fp8(const void* E, int64_t v, int32_t d, int32_t dtype, int64
 int check_logits_fp8(const void* h8, int64_t ldh, const void* h_scale, int64_t lds, int32_t rows,
                      const void* E8, int64_t lde, const void* E_scale, int64_t ldes, int64_t v,
                      int32_t d, const void* out, int32_t out_dtype, int64_t ldo);
+bool verify_fits(int64_t rows, int32_t B, int64_t v);  // v in [1, 2^31)
 int check_verify(const void* logits, int64_t rows, int64_t v, int32_t dtype, int64_t ldl,
                  const void* row_start, int32_t B, const void* draft_tokens, int64_t n_drafts,
                  const void* draft_probs, int64_t ldq, int32_t mode, float tau,
