@@ -356,7 +356,10 @@ int flashhead_rmsnorm(const void* x, int64_t ldx, const void* residual, int64_t 
  *   E        device, v x d, dtype FH_DTYPE_*, 16-byte rows as for dense_head
  *   E8       device, v x d codes, aligned as y8 above
  *   E_scale  device, ceil(v / 128) x ceil(d / 128)
- * No overlap is allowed.  v <= 65535 * 128.
+ * No overlap is allowed.  v <= 65535 * 128.  A NaN gets the NaN code and takes no
+ * part in its block's maximum.  An infinity gets it too and makes its block's
+ * scale infinite and the block's other codes zero: none of that block's values
+ * can be read back.
  */
 int flashhead_quantize_fp8(const void* E, int64_t v, int32_t d, int32_t dtype, int64_t lde,
                            uint8_t* E8, int64_t lde8, float* E_scale, int64_t lds, void* stream);
@@ -367,7 +370,8 @@ int flashhead_quantize_fp8(const void* E, int64_t v, int32_t d, int32_t dtype, i
  *   out[m, t] = sum over k of h8[m, k] h_scale[m, k / 128]
  *                             * E8[t, k] E_scale[t / 128, k / 128]
  * with exact products of two codes and fp32 sums, rounded once to out_dtype.
- * Codes of the e4m3 NaN make the outputs of their row NaN.
+ * Codes of the e4m3 NaN make the outputs of their row NaN.  The product of the
+ * two scales of a block is an fp32 number: below 2^-126 it loses digits.
  *   h8, h_scale   device, rows x d and rows x ceil(d / 128)
  *   E8, E_scale   device, v x d and ceil(v / 128) x ceil(d / 128)
  *   d             a multiple of 16;  v <= 2^28;  rows <= 65535 * 16;  strides
@@ -415,11 +419,12 @@ int dense_logits_fp8(const uint8_t* h8, int64_t ldh, const float* h_scale, int64
  *                 outside every sequence are not used)
  *   draft_tokens  device, n_drafts
  *   draft_probs   device, n_drafts x v fp32 (>= 0, rows at multiples of 16
- *                 bytes), or NULL; NULL in greedy mode.  A NaN counts as a
- *                 weight of 0.
+ *                 bytes), or NULL; NULL in greedy mode.  A draft whose q is a
+ *                 NaN is not accepted, and a token whose q is a NaN is not
+ *                 drawn from max(p - q, 0).
  *   u_accept      device, n_drafts fp32 in [0, 1); u_sample device, B fp32 in
  *                 [0, 1); both may be NULL in greedy mode
- *   tau           finite, > 0 (greedy: not used)
+ *   tau           finite, > 0, the fp32 number itself (greedy: not used)
  *   max_tokens    columns of out_tokens and out_logp
  *   out_tokens    device, B x max_tokens: the accepted drafts, then the next
  *                 token, then -1
