@@ -214,6 +214,51 @@ int check_logits_fp8(const void* h8, int64_t ldh, const void* h_scale, int64_t l
   return FH_OK;
 }
 
+namespace {
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+}  // namespace
+
+Logits8Plan plan_logits8(int64_t rows, int64_t v, int32_t d, int64_t ldo, int out_size) {
+  if (rows <= 16) {
+    // As many rows of E a workgroup as leave most compute units one (1 x 4000
+    // x 4096: 7 us with 16, 9 with 32; 16 x 32000 x 2048: 14 us with 64, 21
+    // with 16); one row of h gains nothing from more than 32.
+    if (v > 64 * 192 && rows > 4) return {false, 16, 64};
+    return {false, 16, v > 32 * 192 ? 32 : 16};
+  }
+  // Estimated times in us.  Four waves with 32 rows of h and 64 of E, two
+  // workgroups a compute unit: 2 us, 2.2 us for four blocks of columns, and E
+  // once at the memory's rate (for 672 x 1424 x 560: 6 us, 8 with the smallest
+  // tiles).
+  const int64_t blocks = ceil_div(d, 128);
+  Logits8Plan plan{false, 32, 64};
+  double best = 2.0 +
+                2.2 * (double)(ceil_div(ceil_div(rows, 32) * ceil_div(v, 64), 2 * kLogits8Groups) *
+                               ceil_div(blocks, kLogits8Split)) +
+                (double)v * d / 5.4e6;
+  // Tiles: 3 us, and for each round of workgroups and each block the measured
+  // time of a block (333 x 5003 x 1104, 64 x 16000 x 2048 and 40 x 20000 x 1024
+  // with each tile; a smaller tile has more workgroups and less to do in each).
+  static const struct {
+    int bm, bn;
+    double block;
+  } kTiles[] = {{64, 128, 0.86}, {128, 128, 1.24}, {64, 256, 1.31}, {128, 256, 1.81}};
+  // (the tiles reach 128 rows of out by 31-bit offsets)
+  if (ldo * out_size < 1 << 23)
+    for (const auto& t : kTiles) {
+      const int64_t rounds =
+          ceil_div(ceil_div(rows, t.bm) * ceil_div(v, t.bn), kLogits8Groups);
+      const double time = 3.0 + (double)(rounds * blocks) * t.block;
+      if (time < best) {
+        best = time;
+        plan = Logits8Plan{true, t.bm, t.bn};
+      }
+    }
+  return plan;
+}
+
 bool verify_fits(int64_t rows, int32_t B, int64_t v) {
   // chunks of 2048 values; 512 threads a sequence
   const int64_t chunks = (v + 2047) / 2048;

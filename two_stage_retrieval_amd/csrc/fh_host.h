@@ -49,6 +49,17 @@ void quantize_int4(const uint16_t* C, const double* shift, int c, int d,
                    std::vector<uint8_t>& codes, std::vector<uint16_t>& scales, int* ntiles_out,
                    int* groups_out);
 
+// The kernel of a dense_logits_fp8 call: tiles of bm rows of h by bn of E, which
+// kLogits8Groups workgroups take one after the other, or (few rows, or few
+// tiles) a workgroup for every bm x bn, whose kLogits8Split waves share d.
+constexpr int kLogits8Groups = 256;  // compute units
+constexpr int kLogits8Split = 4;
+struct Logits8Plan {
+  bool tiles;
+  int bm, bn;
+};
+Logits8Plan plan_logits8(int64_t rows, int64_t v, int32_t d, int64_t ldo, int out_size);
+
 // The row stride that a call uses of an optional matrix: 0 where no second row
 // is there (such a stride may hold anything).
 int64_t row_stride(const void* p, int64_t ld, int64_t rows);

@@ -5,6 +5,7 @@
 // the matrix cores; its fp32 result is then scaled and added to the fp32
 // accumulator, since the scales change from block to block.
 #include "fh_device.h"
+#include "fh_host.h"
 #include "fh_internal.h"
 
 namespace fh {
@@ -162,7 +163,7 @@ __device__ __forceinline__ void load_lds_wait() {
 // product of these sizes, without the scales and with E already in bf16, 943).
 // The matrix instructions fill 489 us at 2.1 GHz; between them are the
 // conversions of both operands, the LDS reads and the sums.
-constexpr int kTileGroups = 256;  // compute units
+constexpr int kTileGroups = kLogits8Groups;
 
 template <int kBM, int kBN, typename TO>
 __global__ __launch_bounds__(512, 2) void logits8_tiles_kernel(const Logits8Args a) {
@@ -460,7 +461,7 @@ __global__ __launch_bounds__(512, 2) void logits8_tiles_kernel(const Logits8Args
 // us (5.9 TB/s; a plain read of 1 GiB reaches 5.5, part of E stays in the
 // memory-side cache).
 // ---------------------------------------------------------------------------
-constexpr int kSplit = 4;
+constexpr int kSplit = kLogits8Split;
 
 template <int MT, int NT, typename TO>
 __global__ __launch_bounds__(256, 2) void logits8_rows_kernel(const Logits8Args a) {
@@ -560,61 +561,23 @@ void enqueue_tiles(const Logits8Args& a, hipStream_t s) {
   hipLaunchKernelGGL((logits8_tiles_kernel<kBM, kBN, TO>), dim3(kTileGroups), dim3(512), 0, s, a);
 }
 
-// Estimated times in us.  Tiles: 3 us, and for each round of workgroups and
-// each block of columns the measured time of a block (333 x 5003 x 1104, 64 x
-// 16000 x 2048 and 40 x 20000 x 1024 with each tile; a smaller tile has more
-// workgroups and less to do in each).
-struct TileTime {
-  int bm, bn;
-  double block;
-};
-constexpr TileTime kTileTimes[] = {
-    {64, 128, 0.86}, {128, 128, 1.24}, {64, 256, 1.31}, {128, 256, 1.81}};
-double rounds(int64_t groups, int at_once) { return (double)((groups + at_once - 1) / at_once); }
-double tiles_time(const Logits8Args& a, const TileTime& t) {
-  const int64_t tiles = (int64_t)((a.rows + t.bm - 1) / t.bm) * ((a.v + t.bn - 1) / t.bn);
-  return 3.0 + rounds(tiles, kTileGroups) * ((a.d + 127) / 128) * t.block;
-}
-// Four waves with 32 rows of h and 64 of E, two workgroups a compute unit: 2 us,
-// 2.2 us for four blocks, and E once at the memory's rate (for 672 x 1424 x
-// 560: 6 us, 8 with the smallest tiles).
-double few_time(const Logits8Args& a) {
-  const int64_t groups = (int64_t)((a.rows + 31) / 32) * ((a.v + 63) / 64);
-  return 2.0 + rounds(groups, 2 * kTileGroups) * (((a.d + 127) / 128 + kSplit - 1) / kSplit) * 2.2 +
-         (double)a.v * a.d / 5.4e6;
-}
-
 template <typename TO>
 void enqueue(const Logits8Args& a, hipStream_t s) {
-  if (a.rows <= 16) {
-    // As many rows of E a workgroup as leave most compute units one (1 x 4000
-    // x 4096: 7 us with 16, 9 with 32; 16 x 32000 x 2048: 14 us with 64, 21
-    // with 16); one row of h gains nothing from more than 32.
-    if (a.v > 64 * 192 && a.rows > 4)
-      enqueue_rows<1, 4, TO>(a, s);
-    else if (a.v > 32 * 192)
-      enqueue_rows<1, 2, TO>(a, s);
-    else
-      enqueue_rows<1, 1, TO>(a, s);
+  const Logits8Plan p = plan_logits8(a.rows, a.v, a.d, a.ldo, sizeof(TO));
+  if (p.tiles) {
+    switch (p.bm * 1000 + p.bn) {
+      case 64128: enqueue_tiles<64, 128, TO>(a, s); break;
+      case 128128: enqueue_tiles<128, 128, TO>(a, s); break;
+      case 64256: enqueue_tiles<64, 256, TO>(a, s); break;
+      case 128256: enqueue_tiles<128, 256, TO>(a, s); break;
+    }
     return;
   }
-  double best = few_time(a);
-  int tile = -1;
-  // (the tiles reach 128 rows of out by 31-bit offsets)
-  if (a.ldo * (int64_t)sizeof(TO) < 1 << 23)
-    for (int i = 0; i < 4; ++i) {
-      const double t = tiles_time(a, kTileTimes[i]);
-      if (t < best) {
-        best = t;
-        tile = i;
-      }
-    }
-  switch (tile) {
-    case 0: enqueue_tiles<64, 128, TO>(a, s); break;
-    case 1: enqueue_tiles<128, 128, TO>(a, s); break;
-    case 2: enqueue_tiles<64, 256, TO>(a, s); break;
-    case 3: enqueue_tiles<128, 256, TO>(a, s); break;
-    default: enqueue_rows<2, 4, TO>(a, s);
+  switch (p.bm * 1000 + p.bn) {
+    case 16016: enqueue_rows<1, 1, TO>(a, s); break;
+    case 16032: enqueue_rows<1, 2, TO>(a, s); break;
+    case 16064: enqueue_rows<1, 4, TO>(a, s); break;
+    case 32064: enqueue_rows<2, 4, TO>(a, s); break;
   }
 }
 
