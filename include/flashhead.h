@@ -395,9 +395,10 @@ int dense_logits_fp8(const uint8_t* h8, int64_t ldh, const float* h_scale, int64
  * row_start[s]) holds no sequence and may be anywhere in the batch.  The
  * drafts of all sequences are one after the other in draft_tokens, draft_probs
  * and u_accept: the j-th of sequence s is entry row_start[s] - (sequences
- * before s that have a row) + j.  (Arrays too short to hold them so are read as
- * if every slot before s had a row.)  With p_j = softmax(logits / tau) at its
- * row,
+ * before s that have a row) + j (row_start[0] is 0 as a rule; with another one
+ * the arrays begin with as many entries that no sequence has).  Arrays too short
+ * to hold them so are read as if every slot before s had a row.  With p_j =
+ * softmax(logits / tau) at its row,
  *   sample   draft x_j is accepted while u_accept[j] q_j(x_j) < p_j(x_j),
  *            q_j its row of draft_probs, or 1 at x_j and 0 elsewhere when
  *            draft_probs is NULL (a draft chosen without chance).  At the
@@ -439,7 +440,7 @@ int dense_logits_fp8(const uint8_t* h8, int64_t ldh, const float* h_scale, int64
  *                 contents need no initialisation, and one made for more
  *                 sequences or rows serves fewer.
  * FH_ERR_INVALID_ARG for a workspace that is too small; FH_ERR_UNSUPPORTED
- * where rows or B times ceil(v / 2048) reach 2^24 - 1, or B reaches 2^23
+ * where rows or B times ceil(v / 2048) reach 2^24, or B reaches 2^23
  * (workspace_bytes is 0 for sizes that the call refuses).
  */
 size_t flashhead_verify_workspace_bytes(int32_t B, int64_t rows, int64_t v);

@@ -1,5 +1,5 @@
-// Host-only checks and the INT4 centroid quantizer (declarations and their
-// contracts in fh_host.h).
+// Host-only checks, the INT4 centroid quantizer and the choice of the 8-bit
+// logits' kernel (declarations and their contracts in fh_host.h).
 #include "fh_host.h"
 
 #include <math.h>

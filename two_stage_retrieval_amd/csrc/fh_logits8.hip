@@ -159,10 +159,11 @@ __device__ __forceinline__ void load_lds_wait() {
 // ahead.  This goes on over the ends of tiles, and a tile's stores are behind
 // the loads of the next one's first block, so that neither stands alone.
 //
-// 2048 x 128256 x 2048 to bf16 takes 1054 us (1.02 PFLOP/s; a library's bf16
-// product of these sizes, without the scales and with E already in bf16, 943).
-// The matrix instructions fill 489 us at 2.1 GHz; between them are the
-// conversions of both operands, the LDS reads and the sums.
+// 2048 x 128256 x 2048 to bf16 takes 1012 to 1054 us (1.02 to 1.06 PFLOP/s; a
+// library's bf16 product of these sizes, without the scales and with E already in
+// bf16, 943), to fp32 1080.  The matrix instructions fill 489 us at 2.1 GHz (43 %
+// busy); between them are the conversions of both operands, the LDS reads and
+// the sums.
 constexpr int kTileGroups = kLogits8Groups;
 
 template <int kBM, int kBN, typename TO>

@@ -81,8 +81,8 @@ constexpr float kSmallMean = 7.88860905e-31f;  // 2^-100
 // kRowThreads threads per row (a wave, four rows a workgroup, or the whole
 // workgroup); the row stays in registers between the sum and the outputs, so x
 // may be y and r may be the residual's output.  Bound by memory: 8192 rows of
-// 2048 bf16 with the residual, to 8 bits, take 24.4 us for 118 MB (4.8 TB/s; a
-// large copy reaches 5.1).
+// 2048 bf16 with the residual, to 8 bits, take 25.6 to 28.3 us for 118 MB (4.2 to
+// 4.6 TB/s; a large copy reaches 5.1), of fp32 44 us for 219 MB (5.0).
 template <typename T, int kRowThreads, int kUnits>
 __global__ __launch_bounds__(kNormThreads) void rmsnorm_kernel(const RmsnormArgs a) {
   constexpr int N = Unit<T>::kElems;
@@ -188,7 +188,7 @@ __global__ __launch_bounds__(kNormThreads) void rmsnorm_kernel(const RmsnormArgs
 }
 
 // One workgroup per 128 x 128 block, held in registers between the maximum
-// and the codes.  Bound by memory: 128256 x 2048 bf16 take 148 us for 788 MB
+// and the codes.  Bound by memory: 128256 x 2048 bf16 take 149 us for 788 MB
 // (5.3 TB/s), with IEEE divisions.
 template <typename T>
 __global__ __launch_bounds__(256) void quantize_fp8_kernel(const QuantizeFp8Args a) {

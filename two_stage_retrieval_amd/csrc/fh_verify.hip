@@ -20,10 +20,10 @@
 // chunk's running sum the token.  Only max(p - q, 0) has other chunk sums than
 // p: then a workgroup per chunk sums the chunk's weights, and the sequence's
 // last one draws.  Those decide for themselves in the second launch where
-// they all fit the device at once (one sequence of four drafts, 128256: 5 + 8
+// they all fit the device at once (one sequence of four drafts, 128256: 5 + 9
 // us); where they do not, a third launch takes over the second's state (64
-// sequences: 31 + 9 + 16 us; with the same decisions made by every chunk's
-// workgroup the second launch took 41).
+// sequences: 31 + 8 + 18 us; with the same decisions made by every chunk's
+// workgroup the second launch took 41).  Greedy decoding of as many rows: 31 + 5.
 #include "fh_device.h"
 #include "fh_internal.h"
 
@@ -145,7 +145,8 @@ __device__ __forceinline__ void count_empty(const VerifyArgs& a, int w, int lane
   auto none = [&](int64_t s) { return s < to && a.row_start[s + 1] <= a.row_start[s]; };
   int count = 0;
 #pragma unroll 4
-  for (int64_t s = from; s < to; s += kWave) count += __builtin_popcountll(__ballot(none(s + lane)));
+  for (int64_t s = from; s < to; s += kWave)
+    count += __builtin_popcountll(__ballot(none(s + lane)));
   if (lane == 0) s_count[w] = count;
   __syncthreads();
   int before = 0, total = 0;
@@ -574,6 +575,10 @@ void enqueue(const VerifyArgs& a, hipStream_t s) {
     hipLaunchKernelGGL((verify_rows_kernel<T, false>), rows, dim3(kVThreads), 0, s, a);
   else if (a.rows)
     hipLaunchKernelGGL((verify_rows_kernel<T, true>), rows, dim3(kVThreads), 0, s, a);
+  // Two workgroups a compute unit fit the device at once.  Calls with two and
+  // with three launches, us: 8 sequences of 128256 (504 workgroups) 18.0 and 21.3,
+  // 16 (1008) 22.7 and 24.9, 32 (2016) 31.7 and 29.0; 32 of 32000 (512) 17.2 and
+  // 20.9, 40 (640) 22.1 and 21.5, 128 (2048) 49 and 29.
   if (a.q && (int64_t)B * n <= 512) {
     hipLaunchKernelGGL((verify_decide_kernel<T, kAll>), dim3(B * n), dim3(kDecideThreads), 0, s, a);
     return;
