@@ -59,7 +59,7 @@ def test_an_object_dropped_while_a_call_is_queued(fh):
         del own
         torch.cuda.synchronize()
         with torch.cuda.stream(side):
-            torch.cuda._sleep(100_000_000)      # some ten ms, then the calls
+            torch.cuda._sleep(300_000_000)      # 0.1 s and more, then the calls
         z = head.logits(x, stream=side.cuda_stream)
         got = head.verify(x, st, drafts, 2, mode=fh.FH_MODE_GREEDY, stream=side.cuda_stream)
         del head
