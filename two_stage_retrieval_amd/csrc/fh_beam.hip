@@ -34,31 +34,29 @@ __device__ __forceinline__ bool goes_on(const BeamArgs& a, int64_t r) {
   return fabsf(a.scores[r]) < INFINITY && !(a.finished && a.finished[r]);
 }
 
-// max(a, b, c), and max(a, b), of numbers from memory in one instruction (fmaxf
-// takes another for each of them, against signalling NaNs, which the row's test finds
-// as well)
+// max(a, b, c) of numbers from memory in one instruction (fmaxf takes another for
+// each of them, against signalling NaNs, which the row's test finds as well)
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
   return r;
 }
 
-__device__ __forceinline__ float max2(float a, float b) {
-  float r;
-  asm("v_max_f32 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
-  return r;
-}
-
-// exp(x - top) for less <= x, as 2^n 2^f with n the nearest whole number to y = (x -
+// exp(x - top) for x <= top, as 2^n 2^f with n the nearest whole number to y = (x -
 // top) log2(e), which the low word of a sum with 1.5 * 2^52 holds; 2^f is 1 + f r(f),
 // r the polynomial that interpolates (2^f - 1) / f at the seven Chebyshev nodes of
 // [-1/2, 1/2].  The sums are off by 1.1e-10 at most, which changes the order of two
-// candidates whose scores are as near as that, one in 1e8 neighbours.  Smaller x
-// count as `less` = top - 700.  The instructions set the time of the launch (256
-// rows of 128256: the conversion to fp64 counts as four of the 21 a value).
-__device__ __forceinline__ double weight_near(float x, float less, double top_k) {
-  const double y = fma((double)max2(x, less), kLog2e, -top_k);
-  const double n = y + 6755399441055744.0, f = y - (n - 6755399441055744.0);
+// candidates whose scores are as near as that, one in 1e8 neighbours.  The difference
+// comes first and is cut at -700, both in fp64: logits are as large as fp32 holds,
+// and neither top - 700 as an fp32 number nor the rounding of top log2(e) is small
+// beside a whole number then (from 2^31 on the first left the exponent's field).  The
+// instructions set the time of the launch (256 rows of 128256: the conversion to fp64
+// counts as four of the 21 a value; the same bits put together by shifts take longer,
+// 27 us for 26).
+__device__ __forceinline__ double weight_near(float x, float top) {
+  const double d = fmax((double)x - (double)top, -700.0);
+  const double n = fma(d, kLog2e, 6755399441055744.0);
+  const double f = fma(d, kLog2e, 6755399441055744.0 - n);
   double p = 1.52973237607010755e-05;
   p = fma(p, f, 1.54614446985691293e-04);
   p = fma(p, f, 1.33335023861627698e-03);
@@ -114,7 +112,7 @@ __global__ __launch_bounds__(kRowThreads) void beam_rows_kernel(const BeamArgs a
     for (int i = 0; i < kBlocks; ++i)
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        part[j & 1] += weight_near(x[i][j], top - 700.0f, (double)top * kLog2e);
+        part[j & 1] += weight_near(x[i][j], top);
     sum = wave_sum_f64(part[0] + part[1]);
   }
   if (lane == 0) {
