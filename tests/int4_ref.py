@@ -115,7 +115,8 @@ def beam(logits, scores, finished, n, pad, eos):
             top = row.max()
             if not np.isfinite(top):   # a NaN makes it one
                 continue
-            key = row + (at[b, k] - (top + np.log(np.exp(row - top).sum())))
+            # (a logarithm added to a large top would leave nothing of it, or of `at`)
+            key = at[b, k] + ((row - top) - np.log(np.exp(row - top).sum()))
             t = np.nonzero(row > -np.inf)[0]
             keys.append(key[t])
             places.append(k * v + t)

@@ -1,11 +1,15 @@
 // Beam search's selection over beams and vocabulary, and the reordering of the
 // beams' states.  A candidate (k, t) of a sequence has the score
 //   score_k + z_kt - log(sum_u exp(z_ku)),
-// and the n candidates with the largest are wanted, in order.
+// and the n candidates with the largest are wanted, in order.  With top_k the
+// row's largest logit it is taken as
+//   (z_kt - top_k) + (score_k - log(sum_u exp(z_ku - top_k))):
+// a row of very large logits (one masked by the type's lowest value throughout) would
+// absorb score_k and the logarithm otherwise, and such a beam come before all others.
 //
 // First launch, per (row, chunk): the sum of exponentials and the largest value
 // of each block.  Second, per sequence: a row's chunks are joined, which gives
-// what a row adds to its logits, and with it the score of each block's largest
+// both constants of a row, and with them the score of each block's largest
 // value.  In the order of scores and, of equal ones, of places, every one of
 // the n best candidates lies in one of the n blocks whose largest values are
 // the n best: a block outside them has n candidates before all of its own.  So
@@ -334,10 +338,14 @@ __device__ __forceinline__ int best_of(SelectShared& s, Fill fill, At place, int
 template <typename T>
 __global__ __launch_bounds__(kSelThreads) void beam_select_kernel(const BeamArgs a) {
   __shared__ SelectShared s;
-  __shared__ double s_add[FH_MAX_BEAMS];    // what a row adds to its logits
+  struct __align__(16) Row {
+    double top, rest;   // its largest logit; its score less the sum's logarithm
+    __device__ __forceinline__ double score(float x) const { return ((double)x - top) + rest; }
+  };
+  __shared__ Row s_row[FH_MAX_BEAMS];
   __shared__ uint8_t s_kind[FH_MAX_BEAMS];  // 0 no candidate, 1 its logits, 2 has ended
   struct Block {
-    double add;
+    Row row;
     int64_t first;   // its first token
     int beam, kind;
   };
@@ -389,7 +397,7 @@ __global__ __launch_bounds__(kSelThreads) void beam_select_kernel(const BeamArgs
     if (lane == 0) {
       const bool there = fabsf(score) < INFINITY;
       s_kind[k] = (uint8_t)(!there ? 0 : ended ? 2 : total > 0.0 ? 1 : 0);   // (NaN: none)
-      s_add[k] = ended ? (double)score : (double)score - ((double)top + log(total));
+      s_row[k] = ended ? Row{0.0, (double)score} : Row{(double)top, (double)score - log(total)};
     }
   }
   __syncthreads();
@@ -417,18 +425,18 @@ __global__ __launch_bounds__(kSelThreads) void beam_select_kernel(const BeamArgs
       },
       [&](int b, int j, float x) {
         const int i = (b * kKeep + j) * kSelThreads + tid;
-        return place_of(s_add[beam_of(i)] + (double)x, (uint32_t)i);
+        return place_of(s_row[beam_of(i)].score(x), (uint32_t)i);
       },
       (per + kKeep - 1) / kKeep, per < kKeep ? per : kKeep, a.n_out, w, lane);
   if (tid < blocks) {
     const int i = (int)s.out[tid].at, k = beam_of(i);
-    s_block[tid] = Block{s_add[k], (int64_t)(i - k * (int)nblk) * kBeamBlock, k, s_kind[k]};
+    s_block[tid] = Block{s_row[k], (int64_t)(i - k * (int)nblk) * kBeamBlock, k, s_kind[k]};
   }
   __syncthreads();
 
   // their values: a block a wave, 8 in a row a lane
   static_assert(kBeamBlock == kWave * kKeep, "a block a wave");
-  Block now{0.0, 0, 0, 0};
+  Block now{{0.0, 0.0}, 0, 0, 0};
   const int found = best_of(
       s,
       [&](int b, float* x) {
@@ -446,7 +454,7 @@ __global__ __launch_bounds__(kSelThreads) void beam_select_kernel(const BeamArgs
       [&](int, int j, float x) {
         const uint32_t t =
             now.kind == 2 ? (uint32_t)a.pad_token : (uint32_t)now.first + lane * kKeep + j;
-        return place_of(now.add + (double)x, (uint32_t)(now.beam * a.v) + t);
+        return place_of(now.row.score(x), (uint32_t)(now.beam * a.v) + t);
       },
       (blocks + kSelWaves - 1) / kSelWaves, kKeep, a.n_out, w, lane);
   if (tid < a.n_out) {
