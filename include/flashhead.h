@@ -535,8 +535,9 @@ int dense_logits_int4(const void* h, int64_t ldh, int32_t h_dtype, int32_t rows,
  * (a logit of -inf is no candidate); a beam that has ended has one candidate,
  * pad_token at its own score, and its logits are not read.  The n_out
  * candidates of a sequence with the largest scores come out in that order; of
- * equal ones first the lower beam, then the lower token.  The sums and scores
- * are in fp64, rounded once to out_scores.
+ * equal ones first the lower beam, then the lower token.  The sums (their
+ * terms within 4e-14 of theirs) and scores are in fp64, relative to a row's
+ * largest logit, and rounded once to out_scores.
  *   logits        device, B K x v, FH_DTYPE_*, rows at multiples of 16 bytes (v
  *                 itself may be any size).  A row of -inf alone, or with a NaN
  *                 or +inf, has no candidate.

@@ -20,7 +20,8 @@
 //
 // The sums are in fp64: which of two beams' candidates comes first hangs on
 // the difference of their sums, and fp32 sums are off by 1e-7, which in a batch
-// with thousands of neighbouring candidates a second shows.
+// with thousands of neighbouring candidates a second shows.  (The weights are within
+// 4e-14 of theirs.)
 #include "fh_device.h"
 #include "fh_internal.h"
 #include "fh_weights.h"
@@ -46,36 +47,12 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
-// exp(x - top) for x <= top, as 2^n 2^f with n the nearest whole number to y = (x -
-// top) log2(e), which the low word of a sum with 1.5 * 2^52 holds; 2^f is 1 + f r(f),
-// r the polynomial that interpolates (2^f - 1) / f at the seven Chebyshev nodes of
-// [-1/2, 1/2].  The sums are off by 1.1e-10 at most, which changes the order of two
-// candidates whose scores are as near as that, one in 1e8 neighbours.  The difference
-// comes first and is cut at -700, both in fp64: logits are as large as fp32 holds,
-// and neither top - 700 as an fp32 number nor the rounding of top log2(e) is small
-// beside a whole number then (from 2^31 on the first left the exponent's field).  The
-// instructions set the time of the launch (256 rows of 128256: the conversion to fp64
-// counts as four of the 21 a value; the same bits put together by shifts take longer,
-// 27 us for 26).
-__device__ __forceinline__ double weight_near(float x, float top) {
-  const double d = fmax((double)x - (double)top, -700.0);
-  const double n = fma(d, kLog2e, 6755399441055744.0);
-  const double f = fma(d, kLog2e, 6755399441055744.0 - n);
-  double p = 1.52973237607010755e-05;
-  p = fma(p, f, 1.54614446985691293e-04);
-  p = fma(p, f, 1.33335023861627698e-03);
-  p = fma(p, f, 9.61805667852463735e-03);
-  p = fma(p, f, 5.55041088390961848e-02);
-  p = fma(p, f, 2.40226509222887574e-01);
-  p = fma(p, f, 6.93147180559945286e-01);
-  p = fma(p, f, 1.0);
-  return __hiloint2double(__double2hiint(p) + (__double2loint(n) << 20), __double2loint(p));
-}
-
 // A wave per (row, chunk); a lane holds 8 values of each block.  A NaN or +inf
 // makes the sum NaN; a chunk of -inf alone has sum 0.  256 rows of 128256 in bf16
-// take 26 us (66 MB, 12 us at a copy's rate); sums that start with the first block
-// to arrive, relative to the largest value so far, change nothing.
+// take 28 us (66 MB, 12 us at a copy's rate), which the weights' instructions set:
+// with two terms less, 1e-10 off, 26; with the fp64 numbers put together by shifts
+// instead of converted 29.  Sums that start with the first block to arrive, relative
+// to the largest value so far, change nothing.
 template <typename T>
 __global__ __launch_bounds__(kRowThreads) void beam_rows_kernel(const BeamArgs a) {
   const int lane = threadIdx.x & 63;
@@ -116,7 +93,7 @@ __global__ __launch_bounds__(kRowThreads) void beam_rows_kernel(const BeamArgs a
     for (int i = 0; i < kBlocks; ++i)
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        part[j & 1] += weight_near(x[i][j], top);
+        part[j & 1] += weight<false>(x[i][j], top, kLog2e, -1020.0 / kLog2e);
     sum = wave_sum_f64(part[0] + part[1]);
   }
   if (lane == 0) {
