@@ -33,7 +33,8 @@ __device__ __forceinline__ void load_row8(const uint8_t* p, float* x) {
   }
 }
 
-// Largest and smallest of three in one instruction (a NaN is left out).
+// Largest and smallest of three in one instruction.  (A quiet NaN is left out; a
+// signalling one comes out quiet, and with it what was largest until then is lost.)
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
@@ -143,6 +144,15 @@ __global__ __launch_bounds__(256) void quantize_int4_kernel(const QuantizeInt4Ar
       nan |= __builtin_isunordered(x[i][j], x[i][j + 1]);
       hi = kZero ? max3(hi, x[i][j], x[i][j + 1]) : max3_abs(hi, x[i][j], x[i][j + 1]);
       if constexpr (kZero) lo = min3(lo, x[i][j], x[i][j + 1]);
+    }
+    if (nan) {
+      hi = lo = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float y = x[i][j] == x[i][j] ? x[i][j] : 0.0f;
+        hi = fmaxf(hi, kZero ? y : fabsf(y));
+        if constexpr (kZero) lo = fminf(lo, y);
+      }
     }
     hi = group_max<kLanes>(hi);
     if constexpr (kZero) {
