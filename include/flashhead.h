@@ -510,8 +510,8 @@ int flashhead_int4_rows(const uint8_t* E4, int64_t lde4, const uint16_t* E_scale
  *         bits), 16-byte rows
  *   out   device, rows x v, FH_DTYPE_F32 or FH_DTYPE_BF16, 16-byte rows;
  *         columns [v, ldo) of out are left as they are
- *   rows <= 65535 * 16;  rows * ceil(v / 256) <= 2^29;  strides of h and E4
- *         below 2^22
+ *   rows <= 65535 * 16;  rows * ceil(v / 256) <= 2^29, and for an fp32 h
+ *         ceil(rows / 64) * ceil(v / 2048) < 2^20;  strides of h and E4 below 2^22
  * A row's result does not depend on the other rows' values (their number may
  * change the order of its fp32 sums), and a call is reproducible bit for bit.
  * A NaN or an infinity in a row of h makes that row NaN, and so may values whose

@@ -337,6 +337,23 @@ Logits4Plan plan_logits4(int64_t rows, int64_t v, bool h_f32) {
   return rows <= 16 ? Logits4Plan::kRows16 : Logits4Plan::kRows32;
 }
 
+int64_t logits4_threads(Logits4Plan plan, int64_t rows, int64_t v) {
+  auto tiles = [&](int bm, int bn, int threads) {   // (those of E in eights)
+    return ceil_div(rows, bm) * ceil_div(ceil_div(v, bn), 8) * 8 * threads;
+  };
+  switch (plan) {
+    case Logits4Plan::kRows16: return ceil_div(v, 32) * 512;   // (rows: the second dimension)
+    case Logits4Plan::kRows32: return ceil_div(v, 32) * 256;
+    case Logits4Plan::k16x128: return tiles(16, 128, 256);
+    case Logits4Plan::k32x256: return tiles(32, 256, 256);
+    case Logits4Plan::k48x256: return tiles(48, 256, 256);
+    case Logits4Plan::k64x128: return tiles(64, 128, 256);
+    case Logits4Plan::k64x256: return tiles(64, 256, 512);
+    case Logits4Plan::k64x512: return tiles(64, 512, 512);
+  }
+  return 0;
+}
+
 int check_quantize_int4(const void* E, int64_t v, int32_t d, int32_t dtype, int64_t lde,
                         int32_t group, const void* E4, int64_t lde4, const void* E_scale,
                         const void* E_zero, int64_t lds) {
@@ -371,8 +388,10 @@ int check_logits_int4(const void* h, int64_t ldh, int32_t h_dtype, int32_t rows,
   if (st != FH_OK) return st;
   const int hs = esize_of(h_dtype), os = esize_of(out_dtype);
   if (!hs || !os || rows > 65535 * 16) return FH_ERR_UNSUPPORTED;
-  // fewer than 2^32 threads with each of the tiles (512 for 64 x 256, 256 for 48 x 256)
   if (rows > ((int64_t)1 << 29) / ((v + 255) / 256)) return FH_ERR_UNSUPPORTED;
+  // (only the 64 x 256 tiles of an fp32 h reach it within that)
+  if (rows > 0 && logits4_threads(plan_logits4(rows, v, hs == 4), rows, v) >> 32)
+    return FH_ERR_UNSUPPORTED;
   st = check_rows16(h, ldh, d, hs, rows);
   if (st == FH_OK) st = check_rows16(out, ldo, v, os, rows);
   if (st != FH_OK) return st;

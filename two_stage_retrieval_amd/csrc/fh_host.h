@@ -88,6 +88,8 @@ int check_verify(const void* logits, int64_t rows, int64_t v, int32_t dtype, int
 // the last three others).
 enum class Logits4Plan { kRows16, kRows32, k16x128, k32x256, k48x256, k64x128, k64x256, k64x512 };
 Logits4Plan plan_logits4(int64_t rows, int64_t v, bool h_f32);
+// Threads of its launch along the grid's first dimension, which has 32 bits for them.
+int64_t logits4_threads(Logits4Plan plan, int64_t rows, int64_t v);
 
 // The checks of the calls of the 4-bit head and of beam search.
 int check_quantize_int4(const void* E, int64_t v, int32_t d, int32_t dtype, int64_t lde,
