@@ -505,7 +505,11 @@ int flashhead_int4_rows(const uint8_t* E4, int64_t lde4, const uint16_t* E_scale
  * stand for):
  *   out[m, t] = sum over g of E_scale[g, t] sum over k in g of
  *               (q[t, k] - E_zero[g, t]) h[m, k]
- * with exact products of codes and h, fp32 sums, rounded once to out_dtype.
+ * with exact products of codes and h, fp32 sums, rounded once to out_dtype.  A
+ * group's sum runs from -(24 + E_zero) sum h (24 + E_zero rounded to fp32) over
+ * products of h with 24 + q: its roundings are those of sums of up to (31 +
+ * |E_zero|) sum |h|, whatever h's signs are (2e-7 of the logits' norm at most for
+ * d = 2048, about what a plain fp32 product is off).
  *   h     device, rows x d, h_dtype FH_DTYPE_* (an fp32 h counts with all its
  *         bits), 16-byte rows
  *   out   device, rows x v, FH_DTYPE_F32 or FH_DTYPE_BF16, 16-byte rows;

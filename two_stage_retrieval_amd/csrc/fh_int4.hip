@@ -276,7 +276,11 @@ __global__ __launch_bounds__(256) void int4_rows_kernel(const Int4RowsArgs a, in
 // that the number is 24 + q exactly.  The products with 24 are taken off by the
 // sum of -h, a product of h with -1 that is the same for every row of E:
 //   sum_k (q - zero) h = (24 + zero) sum_k (-h) + sum_k (24 + q) h.
-// Both sums are fp32 sums of exact products.
+// Both sums are fp32 sums of exact products, up to 24 sum |h| large on the way; but
+// the matrix instruction rounds once for several products, so that the logits are about
+// as near as those of a plain fp32 product, for an h of one sign as well (d = 2048, E of
+// normal values: 0.7 to 1.9e-7 of their norm for mixed signs, a plain product 1.0 to
+// 3.4e-7; bf16 h of one sign 1.1 to 4.6e-8 and 0.9 to 3.3e-8).
 
 // The columns of a block of 128 that lane 16 q + . gives to product i: whole
 // groups for the products of a group, and for groups of 128 one load of 16 bytes.
