@@ -898,6 +898,8 @@ class _NormedHead:
         self.v, self.d = E.shape
         if self.d % 16:
             raise ValueError("a width that is a multiple of 16 is expected")
+        if self.d > FH_MAX_NORM_D:
+            raise ValueError(f"a width of {FH_MAX_NORM_D} at most is expected (the norm's)")
         self.eps, self.weight_offset, self.norm_weight = eps, weight_offset, norm_weight
         self.logits_dtype = E.dtype if logits_dtype is None else logits_dtype
         self.max_rows, self.device = max_rows, E.device
