@@ -39,14 +39,6 @@ __device__ __forceinline__ bool goes_on(const BeamArgs& a, int64_t r) {
   return fabsf(a.scores[r]) < INFINITY && !(a.finished && a.finished[r]);
 }
 
-// max(a, b, c) of numbers from memory in one instruction (fmaxf takes another for
-// each of them, against signalling NaNs, which the row's test finds as well)
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
-  return r;
-}
-
 // A wave per (row, chunk); a lane holds 8 values of each block.  A NaN or +inf
 // makes the sum NaN; a chunk of -inf alone has sum 0.  256 rows of 128256 in bf16
 // take 28 us (66 MB, 12 us at a copy's rate), which the weights' instructions set:

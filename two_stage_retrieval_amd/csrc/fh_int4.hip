@@ -4,6 +4,7 @@
 #include "fh_device.h"
 #include "fh_host.h"
 #include "fh_internal.h"
+#include "fh_weights.h"
 
 namespace fh {
 
@@ -18,28 +19,7 @@ typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 // E to 4 bits
 // ---------------------------------------------------------------------------
 
-// 8 columns of a row
-template <typename T>
-__device__ __forceinline__ void load_row8(const uint8_t* p, float* x) {
-  if constexpr (sizeof(T) == 2) {
-    const uint4 w = *reinterpret_cast<const uint4*>(p);
-    x[0] = bf16_lo(w.x); x[1] = bf16_hi(w.x); x[2] = bf16_lo(w.y); x[3] = bf16_hi(w.y);
-    x[4] = bf16_lo(w.z); x[5] = bf16_hi(w.z); x[6] = bf16_lo(w.w); x[7] = bf16_hi(w.w);
-  } else {
-    const float4 a = reinterpret_cast<const float4*>(p)[0];
-    const float4 b = reinterpret_cast<const float4*>(p)[1];
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-  }
-}
-
-// Largest and smallest of three in one instruction.  (A quiet NaN is left out; a
-// signalling one comes out quiet, and with it what was largest until then is lost.)
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
-  return r;
-}
+// The largest |.|, and the smallest, of three, as max3 does.
 __device__ __forceinline__ float max3_abs(float a, float b, float c) {
   float r;
   asm("v_max3_f32 %0, %1, |%2|, |%3|" : "=v"(r) : "v"(a), "v"(b), "v"(c));
@@ -128,7 +108,7 @@ __global__ __launch_bounds__(256) void quantize_int4_kernel(const QuantizeInt4Ar
   for (int i = 0; i < kSteps; ++i) {
     const int64_t r = r0 + i * 16 + in;
     if (cin && r < a.v) {
-      load_row8<T>(a.E + r * a.e_bytes + (int64_t)col * sizeof(T), x[i]);
+      load_whole8<T>(a.E + r * a.e_bytes, col, x[i]);
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) x[i][j] = 0.0f;
@@ -378,7 +358,7 @@ struct RowOfH<float> {
   }
   __device__ __forceinline__ void load(const uint8_t* p) {
     float y[8];
-    load_row8<float>(p, y);
+    load_whole8<float>(p, 0, y);
     split(y);
   }
   __device__ __forceinline__ void clear() {

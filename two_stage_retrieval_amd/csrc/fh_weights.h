@@ -1,5 +1,5 @@
-// Pieces of sums over a row of logits in fp64: loads of either storage type,
-// the weight of a value, and sums over a wave.
+// Loads of rows of either storage type, and pieces of sums over a row of logits in
+// fp64: the weight of a value, and sums over a wave.
 #pragma once
 #include "fh_device.h"
 
@@ -57,6 +57,15 @@ __device__ __forceinline__ double weight(float x, float top, double k, double lo
   p = __hiloint2double(__double2hiint(p) + (__double2loint(n) << 20), __double2loint(p));
   if constexpr (kZero) p = n < 6755399441055744.0 - 1020.0 ? 0.0 : p;
   return p;
+}
+
+// The largest of three numbers from memory in one instruction (fmaxf takes another
+// for each of them).  A quiet NaN is left out; a signalling one comes out quiet, and
+// with it what was largest until then is lost: callers look for NaNs themselves.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+  return r;
 }
 
 // Values [i, i + 8) of a row.
