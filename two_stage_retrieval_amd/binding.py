@@ -979,7 +979,7 @@ class _NormedHead:
         n = K if n_out is None else n_out
         with _made_on(stream):
             if out_scores is None:
-                out_scores = torch.empty(B, n, device=x.device)
+                out_scores = torch.empty(B, n, dtype=torch.float32, device=x.device)
             if out_parents is None:
                 out_parents = torch.empty(B, n, dtype=torch.int32, device=x.device)
             if out_tokens is None:
@@ -1013,9 +1013,10 @@ class DenseHeadFP8(_NormedHead):
         f8 = torch.float8_e4m3fn
         with _made_on(stream):
             self.E8 = torch.empty(self.v, self.d, dtype=f8, device=dev)
-            self.E_scale = torch.empty(-(-self.v // FH_FP8_BLOCK), g, device=dev)
+            self.E_scale = torch.empty(-(-self.v // FH_FP8_BLOCK), g, dtype=torch.float32,
+                                       device=dev)
             self.h8 = torch.empty(max_rows, self.d, dtype=f8, device=dev)
-            self.h_scale = torch.empty(max_rows, g, device=dev)
+            self.h_scale = torch.empty(max_rows, g, dtype=torch.float32, device=dev)
             self.workspace = torch.empty(self._workspace_bytes, dtype=torch.uint8, device=dev)
         flashhead_quantize_fp8(E, self.E8, self.E_scale, stream)
         self._use(stream)
