@@ -1,6 +1,6 @@
 """Runs the 4-bit head, beam selection and the reordering of states for a
 profile: the listed cases of perf/more_operators.py and some more of the same
-ranges, through the library, inputs rotated over two sets.
+ranges, through the library, inputs rotated over three sets.
 
     python3 profiles/int4_beam_cases.py CASES N [--copy]
 
@@ -19,6 +19,13 @@ from perf import more_operators  # noqa: E402
 
 MORE = [
     # forms that the listed cases do not have at these sizes
+    dict(name="pack large f32", op="pack", v=128256, d=2048, dtype="f32", group=128, zero=False),
+    dict(name="logits prompt 64", op="logits", rows=512, v=128256, d=2048, h="bf16", out="bf16",
+         group=64, zero=True),
+    dict(name="logits prompt 32", op="logits", rows=512, v=128256, d=2048, h="bf16", out="bf16",
+         group=32, zero=False),
+    dict(name="logits prompt f32", op="logits", rows=128, v=128256, d=2048, h="f32", out="f32",
+         group=128, zero=False),
     dict(name="logits batch", op="logits", rows=32, v=128256, d=2048, h="bf16", out="bf16",
          group=128, zero=False),
     dict(name="logits drafts", op="logits", rows=64, v=128256, d=2048, h="bf16", out="bf16",
@@ -38,10 +45,10 @@ def main():
     for case in more_operators.listed() + MORE:
         if want != ["all"] and case["name"] not in want:
             continue
-        states = [more_operators.prepare(case, seed) for seed in range(2)]
+        states = [more_operators.prepare(case, seed) for seed in range(3)]
         torch.cuda.synchronize()
         for i in range(n):
-            more_operators.run(states[i % 2])
+            more_operators.run(states[i % 3])
         torch.cuda.synchronize()
         print("ran", case["name"], flush=True)
         del states

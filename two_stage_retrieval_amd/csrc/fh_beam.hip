@@ -41,9 +41,9 @@ __device__ __forceinline__ bool goes_on(const BeamArgs& a, int64_t r) {
 
 // A wave per (row, chunk); a lane holds 8 values of each block.  A NaN or +inf
 // makes the sum NaN; a chunk of -inf alone has sum 0.  256 rows of 128256 in bf16
-// take 28 us (66 MB, 12 us at a copy's rate), which the weights' instructions set:
+// take 29 us (66 MB, 12 us at a copy's rate), which the weights' instructions set:
 // with two terms less, 1e-10 off, 26; with the fp64 numbers put together by shifts
-// instead of converted 29.  Sums that start with the first block to arrive, relative
+// instead of converted 30.  Sums that start with the first block to arrive, relative
 // to the largest value so far, change nothing.
 template <typename T>
 __global__ __launch_bounds__(kRowThreads) void beam_rows_kernel(const BeamArgs a) {

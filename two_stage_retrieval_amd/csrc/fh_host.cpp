@@ -312,14 +312,15 @@ int check_int4(const void* E4, int64_t lde4, const void* E_scale, const void* E_
 
 // The largest tile of which there are enough for three quarters of the compute
 // units (the smallest for an fp32 h: half of them); tiles of h are as even as 64 rows
-// at most allow.  Measured (us; bf16 h, d = 2048): 32 x 128256 39 with 32 x 256 and 48
-// with 16 x 128; 40 x 128256 x 4096 79 with 48 x 256 and 89 with 64 x 512; 64 x 128256
-// 51 with 64 x 512, 60 with 64 x 128 and 87 with 16 x 128, but 64 x 32000 37, 24 and
-// 23, and 64 x 16000 37, 23 and 15.  With fewer workgroups the waves of one share d: 64
-// x 5003 x 1104 7.6 (160 tiles of 16 x 128: 8.6), 1 x 16000 7.4 (11.7); but 1 x 64000 21
-// (15).  h in fp32 (d = 2048): 9 x 128256 51 with 16 x 128, 32 rows 67 with 32 x 256 (16
-// x 128: 87), 128 rows 218 with 64 x 256 (32 x 256: 236); 9 x 20000 27 with 16 x 128, 34
-// with waves that share d, and 9 x 5003 x 1104 15.8 and 10.5.
+// at most allow.  Measured side by side (us a call; bf16 h, d = 2048, groups of 128):
+// 32 x 128256 40 with 32 x 256 and 50 with 16 x 128; 40 x 128256 x 4096 82 with 48 x 256
+// and 85 with 64 x 512; 64 x 128256 50 with 64 x 512, 61 with 64 x 128 and 88 with 16 x
+// 128, but 64 x 32000 37, 24 and 23, and 64 x 16000 37, 23 and 15.  With fewer
+// workgroups the waves of one share d: 64 x 5003 x 1104 7.8 (160 tiles of 16 x 128: 8.8),
+// 1 x 16000 7.6 (11.7); but 1 x 64000 21 (15).  h in fp32 (d = 2048): 32 x 128256 59 with
+// 32 x 256 and 73 with 16 x 128; 128 rows 194 with 64 x 256 and 190 with 32 x 256, but 273
+// and 313 with groups of 32 and zeros; 9 x 20000 19 with 16 x 128, 18 with waves that share
+// d, and 9 x 5003 x 1104 10.7 and 7.5.
 Logits4Plan plan_logits4(int64_t rows, int64_t v, bool h_f32) {
   auto enough = [&](int bm, int bn, int least = 192) {
     return ceil_div(rows, bm) * ceil_div(v, bn) >= least;

@@ -195,7 +195,7 @@ __device__ __forceinline__ float code_at(uint32_t w, int j) {
 
 // A wave takes 8 rows, 8 columns a lane; all that it reads is requested before
 // the first row is written (rows of two dependent reads each would follow one another
-// otherwise).  Bound by memory for rows in a row (128256 x 2048 to bf16: 119 us, 5.5
+// otherwise).  Bound by memory for rows in a row (128256 x 2048 to bf16: 112 us, 5.9
 // TB/s) and, by ids, by the lines that the scales lie in: a token's 2 bytes bring
 // 63 other tokens' with them, once a group.
 constexpr int kReadRows = 8;
@@ -566,13 +566,17 @@ __global__ __launch_bounds__(64 * kSplit) void logits4_rows_kernel(const LogitsI
 // registers, a step ahead, so that every code is read and unpacked once; the rows of
 // h go through LDS (two buffers), and with them the sums of -h, and the scales.
 //
-// Few rows are bound by memory: 1 x 128256 x 2048 takes 29 us for 135 MB (4.6 TB/s),
-// with two blocks at a time, which read whole lines of the codes, and 34 with one.
+// Few rows are bound by memory: 1 x 128256 x 2048 takes 29 us for 135 MB (4.6 TB/s;
+// three or eight such E in turn, more than the caches hold; 25 for two, which they hold
+// in part) with two blocks at a time, which read whole lines of the codes, and 34 with
+// one.
 // For 64 rows and more the unpacking, the scales and the products take turns: 512 x
 // 128256 x 2048 takes 309 to 317 us (0.87 PFLOP/s, the matrix units 35 % busy, four
 // vector instructions for each of theirs; a library's product with E in bf16 271),
-// 64 rows 49 (four tiles of E a wave; 60 with two).  Reads of h from LDS a product
-// ahead, wave priorities around the products, or codes read two steps ahead change 2 %.
+// 64 rows 50 (four tiles of E a wave; 61 with two).  With groups of 32 and zeros 512 rows
+// take 645 (groups of 32 alone 610, of 64 with zeros 417): a product has its own scales
+// then.  Reads of h from LDS a product ahead, wave priorities around the products, or
+// codes read two steps ahead change 2 %.
 // 40 x 262144 x 1152 with groups of 64 and zeros takes 62 (3.4 TB/s); zeros enter where
 // a group's sums start (added at its end: 63.5, and 16 more registers).
 template <int MT, int NT, int W, int S, int kWavesPerSimd, int kGroup, typename TH,
