@@ -70,3 +70,21 @@ def test_scores_do_not_change_with_a_number_added_to_a_row(size):
     check(plain, whole * step, scores, n)
     moved = select(logits, scores, n)
     assert all(torch.equal(a, b) for a, b in zip(plain, moved))
+
+
+@pytest.mark.parametrize("K,v,dtype", [(32, 524288, BF16), (1, 1 << 24, F32), (31, 540671, F32)])
+def test_the_largest_sequences(K, v, dtype):
+    """K * ceil(v / 2048) of 8192 and just below it, the most candidates that there
+    can be, the best ones in the last beam's last tokens."""
+    n = 64
+    logits = padded(K, v, dtype)
+    logits.normal_(generator=gen(K))
+    logits[K - 1, v - 40:] += 9.0
+    scores = torch.linspace(-0.5, 0.0, K, device="cuda")[None].contiguous()
+    out = select(logits, scores, n)
+    key = scores[0].cpu().double()[:, None] + torch.log_softmax(logits.cpu().double(), 1)
+    order = torch.sort(key.view(-1), descending=True, stable=True)[1][:n]
+    assert torch.equal(out[1][0].cpu().long(), order // v)
+    assert torch.equal(out[2][0].cpu().long(), order % v)
+    best = key.view(-1)[order]
+    assert bool(((out[0][0].cpu().double() - best).abs() <= best.abs() * 2.0 ** -24 + 1e-11).all())
